@@ -298,6 +298,106 @@ int32_t moe_nvfp4_route_decode(const moe_nvfp4_args* args, const float* logits, 
 int32_t moe_nvfp4_route_decode_static(const moe_nvfp4_args* args, const float* logits,
                                       const float* bias, hipStream_t stream);
 
+/* ---- FP8 with a scale per block of 128 ------------------------------------------------------
+ *
+ * FP8 checkpoints of mixture-of-experts models keep a weight as E4M3 codes
+ * with one FP32 scale per 128 x 128 block and multiply it with activation rows
+ * quantized to E4M3 with one FP32 scale per 128 consecutive columns (finer
+ * than the one scale per tensor of fp8_skinny_gemm, which the Elsa page's "An
+ * FP8 fast path" describes for attention projections):
+ *   rows     codes uint8 [M][K], scales float [ceil(K/128)][M] (block-major: a
+ *            wavefront reads one block's scales of consecutive rows)
+ *   weights  codes uint8 [G][N][K], scales float [G][ceil(N/128)][ceil(K/128)]
+ *   value = e4m3(code) * scale of its block
+ * The last block of a row or column may be partial. K % 16 == 0 with
+ * 16 <= K <= 65536, 1 <= N <= 2^20, M <= 2^24 rows, 16-byte aligned codes, 4-byte
+ * aligned scales. A call with no rows (M = 0, or R = 0 below) does nothing and
+ * returns NVFP4MOE_OK; its pointers may be NULL.
+ *
+ * Element types of x and y arguments below. */
+#define NVFP4MOE_BF16 0 /* raw BF16 bits, uint16_t */
+#define NVFP4MOE_F32 1  /* float */
+#define NVFP4MOE_FP8 2  /* E4M3 codes with block scales, as above */
+
+/* Quantizes rows. With a = max(largest magnitude of the block, 2^-117):
+ *   scale = a / 448, code = E4M3 nearest to v * (448 / a), ties to even,
+ * every quotient and product one FP32 rounding. swiglu = 0: v = x[m][c], x
+ * [M][K]; swiglu = 1: v = silu(x[m][c]) * x[m][K + c] in FP32, x [M][2K] (gate
+ * half, then up half: what gate_up gives and down takes). Consecutive rows of
+ * x are ldx elements apart (ldx >= the row's columns). x_type BF16 or F32; x
+ * 16-byte aligned, ldx a multiple of 16 bytes. A block that holds an infinity
+ * or a NaN gets a scale that is not finite and the products of its row come
+ * out NaN. One launch. */
+int32_t fp8_quantize_rows(const void* x, int32_t x_type, int64_t M, int64_t K, int64_t ldx,
+                          int32_t swiglu, uint8_t* codes, float* scales, hipStream_t stream);
+
+/* Quantizes weights x [G][N][K] (BF16 or F32, contiguous, 16-byte aligned):
+ * the same recipe over 128 x 128 blocks. G = 0 does nothing. One launch. */
+int32_t fp8_quantize_blocks(const void* x, int32_t x_type, int64_t G, int64_t N, int64_t K,
+                            uint8_t* codes, float* scales, hipStream_t stream);
+
+/* y[m][n] = sum_b xs[b][m] * ws[n / 128][b] * sum_{k in block b} x[m][k] * w[n][k]
+ * for one weight (G = 1). Each block's sum runs on the matrix cores in FP32
+ * and is multiplied by the FP32 product xs * ws (which should be a normal FP32
+ * number: it is formed first); y_type BF16 (one rounding) or F32. With y_type
+ * F32, and for few rows, the codes are multiplied as BF16 values, which is
+ * exact; otherwise by the FP8 instruction, which cuts a product that is small
+ * against the largest of its group of 16 to a multiple of 2^-13 of that one's
+ * power of two (about 10^-4 of y on normal data, well inside its BF16
+ * rounding). M * N <= 2^38. Rows of y are ldy >= N elements apart; elements
+ * between N and ldy are left as they were. The FP32 summation order depends on
+ * the shape and is the same from run to run. One launch. */
+int32_t fp8_block_gemm(const uint8_t* x, const float* x_scales, int64_t M, int64_t K,
+                       const uint8_t* w, const float* w_scales, int64_t N, void* y, int32_t y_type,
+                       int64_t ldy, hipStream_t stream);
+
+/* ---- products grouped by expert ---------------------------------------------------------------
+ *
+ * For every routed pair p = m k + j: y[p] = W_e x[p / pairs_per_row], e the pair's
+ * expert: the expert products of a step or of a prompt, with any N and K and
+ * with BF16 or block-scaled FP8 experts (moe_nvfp4_decode is the whole block on
+ * NVFP4 experts). Groups may have any size, 0 included. pairs_per_row = k
+ * takes token rows (gate_up: x [M]), 1 takes a row per pair (down: x [M k]);
+ * y is in pair order, as moe_combine reads it. */
+typedef struct moe_grouped_args {
+  const void* x;                 /* [x_rows][K]: BF16, or E4M3 codes */
+  const float* x_scales;         /* FP8: [ceil(K/128)][x_rows], else NULL */
+  const void* w;                 /* [E][N][K]: BF16, or E4M3 codes */
+  const float* w_scales;         /* FP8: [E][ceil(N/128)][ceil(K/128)], else NULL */
+  const int32_t* pairs;          /* [R]    from moe_route_topk */
+  const int32_t* active;         /* [E]    from moe_route_topk */
+  const int32_t* active_offsets; /* [E+1]  from moe_route_topk */
+  const int32_t* n_active;       /* [1]    from moe_route_topk */
+  void* y;                       /* [R], rows ldy elements apart */
+  int64_t ldy;
+  int64_t R;                     /* pairs: M k */
+  int64_t x_rows;                /* x_rows * pairs_per_row >= R */
+  int64_t pairs_per_row;
+  int64_t E, N, K;
+  int32_t type;                  /* of x and w: NVFP4MOE_BF16 or NVFP4MOE_FP8 */
+  int32_t y_type;                /* NVFP4MOE_BF16 or NVFP4MOE_F32 */
+} moe_grouped_args;
+
+/* Arithmetic and limits as for fp8_block_gemm, with 1 <= E <= 1024, R < 2^24 and
+ * R * N <= 2^38. The grouping
+ * arrays are read on the device: only the first min(n_active, E, R) slots
+ * count; slot s takes positions active_offsets[s] to active_offsets[s + 1] of
+ * pairs and expert active[s]. Rows of y whose pair no such slot holds are left
+ * as they were (a rank that holds some of the experts passes their slots
+ * only); a pair outside [0, R) or an expert outside [0, E) is skipped. A pair
+ * that appears twice is written twice, in either order. One launch. */
+int32_t moe_grouped_gemm(const moe_grouped_args* args, hipStream_t stream);
+
+/* out[m] = bf16_rne( sum_j w[m][j] * y[m k + j] (+ shared[m]) (+ residual[m]) ), FP32,
+ * in j order, then shared, then residual (the finalize step on its own, for
+ * moe_grouped_gemm's y). y [M k][H] and shared [M][H] (or NULL) of type
+ * y_type, w [M][k], residual BF16 [M][H] (or NULL; may be out). A pair whose
+ * weight is 0 adds nothing, whatever its row of y holds. 1 <= k <= 8,
+ * 1 <= H <= 2^20, M <= 2^24. One launch. */
+int32_t moe_combine(const void* y, int32_t y_type, const float* w, const void* shared,
+                    const uint16_t* residual, int64_t M, int64_t k, int64_t H, uint16_t* out,
+                    hipStream_t stream);
+
 /* ---- read ceiling (measurement) ---------------------------------------------------------
  *
  * The pages judge a decode step by the memory bandwidth it reaches against

@@ -47,6 +47,20 @@ class MoeArgs(ctypes.Structure):
         ("proj_w", _vp), ("proj_n", _i64), ("proj_out", _vp),
     ]
 
+class GroupedArgs(ctypes.Structure):
+    """Mirror of struct moe_grouped_args."""
+    _fields_ = [
+        ("x", _vp), ("x_scales", _vp), ("w", _vp), ("w_scales", _vp), ("pairs", _vp),
+        ("active", _vp), ("active_offsets", _vp), ("n_active", _vp), ("y", _vp), ("ldy", _i64),
+        ("R", _i64), ("x_rows", _i64), ("pairs_per_row", _i64), ("E", _i64), ("N", _i64),
+        ("K", _i64), ("type", _i32), ("y_type", _i32),
+    ]
+
+
+# element types of the block-scaled and grouped calls
+NVFP4MOE_BF16, NVFP4MOE_F32, NVFP4MOE_FP8 = 0, 1, 2
+_FLOAT_TYPES = {torch.bfloat16: NVFP4MOE_BF16, torch.float32: NVFP4MOE_F32}
+
 # moe_nvfp4_args.schedule
 SCHEDULE_AUTO, SCHEDULE_THREE_LAUNCHES, SCHEDULE_TWO_LAUNCHES = 0, 2, 3
 
@@ -86,6 +100,16 @@ def _load():
     L.moe_nvfp4_route_decode.argtypes = [ctypes.POINTER(MoeArgs), _vp, _vp, _vp]
     L.moe_nvfp4_route_decode_static.restype = _i32
     L.moe_nvfp4_route_decode_static.argtypes = [ctypes.POINTER(MoeArgs), _vp, _vp, _vp]
+    L.fp8_quantize_rows.restype = _i32
+    L.fp8_quantize_rows.argtypes = [_vp, _i32, _i64, _i64, _i64, _i32, _vp, _vp, _vp]
+    L.fp8_quantize_blocks.restype = _i32
+    L.fp8_quantize_blocks.argtypes = [_vp, _i32, _i64, _i64, _i64, _vp, _vp, _vp]
+    L.fp8_block_gemm.restype = _i32
+    L.fp8_block_gemm.argtypes = [_vp, _vp, _i64, _i64, _vp, _vp, _i64, _vp, _i32, _i64, _vp]
+    L.moe_grouped_gemm.restype = _i32
+    L.moe_grouped_gemm.argtypes = [ctypes.POINTER(GroupedArgs), _vp]
+    L.moe_combine.restype = _i32
+    L.moe_combine.argtypes = [_vp, _i32, _vp, _vp, _vp, _i64, _i64, _i64, _vp, _vp]
     L.nvfp4moe_stream_blocks.restype = _i64
     L.nvfp4moe_stream_blocks.argtypes = [_i64]
     L.nvfp4moe_stream_read.restype = _i32
@@ -100,7 +124,9 @@ EXPORTS = ["nvfp4moe_strerror", "nvfp4moe_last_error_detail", "nvfp4moe_version"
            "nvfp4_packed_bytes", "nvfp4_pack", "nvfp4_quantize", "nvfp4_dequant_f32", "nvfp4_skinny_gemm",
            "moe_route_topk", "moe_route_project_topk", "moe_nvfp4_workspace_bytes", "moe_nvfp4_decode",
            "moe_nvfp4_route_decode", "moe_nvfp4_route_decode_static", "nvfp4moe_stream_blocks",
-           "nvfp4moe_stream_read"]
+           "nvfp4moe_stream_read",
+           "fp8_quantize_rows", "fp8_quantize_blocks", "fp8_block_gemm", "moe_grouped_gemm",
+           "moe_combine"]
 
 
 def strerror(status: int) -> str:
@@ -471,3 +497,215 @@ def moe_nvfp4_route_decode(x: torch.Tensor, logits: torch.Tensor, k: int,
         _check(lib.moe_nvfp4_route_decode(ctypes.byref(a), _ptr(logits), _ptr(bias),
                                           _stream(stream)), "moe_nvfp4_route_decode")
     return out, ids, w
+
+
+# ---- FP8 with a scale per block of 128, products grouped by expert -----------------------
+
+@dataclass
+class Fp8Rows:
+    """Rows of E4M3 codes with a scale per 128 columns, block-major."""
+    codes: torch.Tensor   # uint8 [M][K]
+    scales: torch.Tensor  # float32 [ceil(K/128)][M]
+
+
+@dataclass
+class Fp8Blocks:
+    """G weights of E4M3 codes with a scale per 128 x 128 block."""
+    codes: torch.Tensor   # uint8 [G][N][K]
+    scales: torch.Tensor  # float32 [G][ceil(N/128)][ceil(K/128)]
+
+
+def _blocks128(n: int) -> int:
+    return (n + 127) // 128
+
+
+class _On:
+    """The device of a call's tensors and the stream it runs on (the given
+    one, or that device's current one), both current while the call allocates
+    its outputs and launches."""
+
+    def __init__(self, t: torch.Tensor, stream):
+        if not t.is_cuda:
+            raise ValueError("expected a GPU tensor")
+        if stream is not None and stream.device != t.device:
+            raise ValueError(f"stream is on {stream.device}, the tensors on {t.device}")
+        self.stream = torch.cuda.current_stream(t.device) if stream is None else stream
+        self._ctx = torch.cuda.stream(self.stream)
+
+    def __enter__(self):
+        self._ctx.__enter__()
+        return self.stream.cuda_stream
+
+    def __exit__(self, *exc):
+        return self._ctx.__exit__(*exc)
+
+
+def _want_rows(t: torch.Tensor, name: str, shape, dtype, device):
+    """As _want, for a matrix whose rows may be further apart than their length."""
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, x on {device}")
+    if t.shape[1] > 1 and t.stride(1) != 1 or t.shape[0] > 1 and t.stride(0) < t.shape[1]:
+        raise ValueError(f"the columns of {name} must be contiguous and its rows apart")
+
+
+def _row_stride(t: torch.Tensor) -> int:
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _float_type(dtype, name: str) -> int:
+    if dtype not in _FLOAT_TYPES:
+        raise ValueError(f"{name} must be bfloat16 or float32, got {dtype}")
+    return _FLOAT_TYPES[dtype]
+
+
+def _want_fp8_rows(x: Fp8Rows):
+    if x.codes.dim() != 2:
+        raise ValueError("row codes must be [M][K]")
+    M, K = x.codes.shape
+    _want(x.codes, "row codes", (M, K), torch.uint8, x.codes.device)
+    _want(x.scales, "row scales", (_blocks128(K), M), torch.float32, x.codes.device)
+    return M, K
+
+
+def _want_fp8_blocks(w: Fp8Blocks, K: int, device):
+    if w.codes.dim() != 3 or w.codes.shape[2] != K:
+        raise ValueError(f"weight codes must be [G][N][{K}], got {list(w.codes.shape)}")
+    G, N, _ = w.codes.shape
+    _want(w.codes, "weight codes", (G, N, K), torch.uint8, device)
+    _want(w.scales, "weight scales", (G, _blocks128(N), _blocks128(K)), torch.float32, device)
+    return G, N
+
+
+def fp8_quantize_rows(x: torch.Tensor, swiglu: bool = False, stream=None,
+                      out: Optional[Fp8Rows] = None) -> Fp8Rows:
+    """x bfloat16 or float32 [M][K] -> E4M3 rows; swiglu: x [M][2K], of
+    silu(x[:, :K]) * x[:, K:]. Rows of x may be strided."""
+    if x.dim() != 2 or (swiglu and x.shape[1] % 2):
+        raise ValueError("x must be [M][K], or [M][2K] with swiglu")
+    xt = _float_type(x.dtype, "x")
+    M, K = x.shape[0], x.shape[1] // 2 if swiglu else x.shape[1]
+    _want_rows(x, "x", x.shape, x.dtype, x.device)
+    with _On(x, stream) as s:
+        if out is None:
+            out = Fp8Rows(torch.empty((M, K), dtype=torch.uint8, device=x.device),
+                          torch.empty((_blocks128(K), M), dtype=torch.float32, device=x.device))
+        _want(out.codes, "out.codes", (M, K), torch.uint8, x.device)
+        _want(out.scales, "out.scales", (_blocks128(K), M), torch.float32, x.device)
+        _check(lib.fp8_quantize_rows(x.data_ptr(), xt, M, K, _row_stride(x), int(swiglu),
+                                     _ptr(out.codes), _ptr(out.scales), s), "fp8_quantize_rows")
+    return out
+
+
+def fp8_quantize_blocks(w: torch.Tensor, stream=None,
+                        out: Optional[Fp8Blocks] = None) -> Fp8Blocks:
+    """w bfloat16 or float32 [G][N][K] (or [N][K]: G = 1) -> E4M3 weights."""
+    wt = _float_type(w.dtype, "w")
+    if w.dim() == 2:
+        w = w.unsqueeze(0)
+    if w.dim() != 3:
+        raise ValueError("w must be [G][N][K] or [N][K]")
+    G, N, K = w.shape
+    with _On(w, stream) as s:
+        if out is None:
+            out = Fp8Blocks(torch.empty((G, N, K), dtype=torch.uint8, device=w.device),
+                            torch.empty((G, _blocks128(N), _blocks128(K)), dtype=torch.float32,
+                                        device=w.device))
+        _want(out.codes, "out.codes", (G, N, K), torch.uint8, w.device)
+        _want(out.scales, "out.scales", (G, _blocks128(N), _blocks128(K)), torch.float32,
+              w.device)
+        _check(lib.fp8_quantize_blocks(_ptr(w), wt, G, N, K, _ptr(out.codes), _ptr(out.scales),
+                                       s), "fp8_quantize_blocks")
+    return out
+
+
+def fp8_block_gemm(x: Fp8Rows, w: Fp8Blocks, out_dtype: torch.dtype = torch.bfloat16,
+                   stream=None, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """x [M][K], w G = 1 [N][K] -> out_dtype [M][N] = x w^T. Rows of out may be strided."""
+    M, K = _want_fp8_rows(x)
+    dev = x.codes.device
+    G, N = _want_fp8_blocks(w, K, dev)
+    if G != 1:
+        raise ValueError("w must hold one matrix")
+    yt = _float_type(out_dtype, "out_dtype")
+    with _On(x.codes, stream) as s:
+        if out is None:
+            out = torch.empty((M, N), dtype=out_dtype, device=dev)
+        _want_rows(out, "out", (M, N), out_dtype, dev)
+        _check(lib.fp8_block_gemm(_ptr(x.codes), _ptr(x.scales), M, K, _ptr(w.codes),
+                                  _ptr(w.scales), N, out.data_ptr(), yt, _row_stride(out), s),
+               "fp8_block_gemm")
+    return out
+
+
+def moe_grouped_gemm(x, routing: Routing, w, out_dtype: torch.dtype = torch.bfloat16,
+                     stream=None, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Products grouped by expert: x bfloat16 [rows][K] with w bfloat16 [E][N][K],
+    or x Fp8Rows with w Fp8Blocks -> out_dtype [M k][N] in pair order. rows is M
+    (token rows: pair p reads row p // k) or M k (pair p reads row p). Rows of
+    out may be strided; those of pairs in no active slot are left as they were."""
+    M, k = routing.ids.shape
+    R = M * k
+    fp8 = isinstance(x, Fp8Rows)
+    if fp8 != isinstance(w, Fp8Blocks):
+        raise ValueError("x and w must both be FP8 (Fp8Rows, Fp8Blocks) or both bfloat16")
+    a = GroupedArgs()
+    if fp8:
+        rows, K = _want_fp8_rows(x)
+        xc, dev = x.codes, x.codes.device
+        E, N = _want_fp8_blocks(w, K, dev)
+        a.x, a.x_scales = _ptr(x.codes), _ptr(x.scales)
+        a.w, a.w_scales = _ptr(w.codes), _ptr(w.scales)
+        a.type = NVFP4MOE_FP8
+    else:
+        if x.dim() != 2 or w.dim() != 3 or x.shape[1] != w.shape[2]:
+            raise ValueError("need x [rows][K] and w [E][N][K]")
+        xc, dev = x, x.device
+        rows, K = x.shape
+        E, N = w.shape[:2]
+        _want(x, "x", (rows, K), torch.bfloat16, dev)
+        _want(w, "w", (E, N, K), torch.bfloat16, dev)
+        a.x, a.w, a.type = _ptr(x), _ptr(w), NVFP4MOE_BF16
+    if rows not in (M, R):
+        raise ValueError(f"x has {rows} rows: need {M} (token rows) or {R} (a row per pair)")
+    for name, t, n in (("pairs", routing.pairs, R), ("active", routing.active, E),
+                       ("active_offsets", routing.active_offsets, E + 1),
+                       ("n_active", routing.n_active, 1)):
+        _want(t, name, (n,), torch.int32, dev)
+    a.pairs, a.active = _ptr(routing.pairs), _ptr(routing.active)
+    a.active_offsets, a.n_active = _ptr(routing.active_offsets), _ptr(routing.n_active)
+    a.R, a.x_rows, a.pairs_per_row = R, rows, 1 if rows == R else k
+    a.E, a.N, a.K = E, N, K
+    a.y_type = _float_type(out_dtype, "out_dtype")
+    with _On(xc, stream) as s:
+        if out is None:
+            out = torch.empty((R, N), dtype=out_dtype, device=dev)
+        _want_rows(out, "out", (R, N), out_dtype, dev)
+        a.y, a.ldy = out.data_ptr(), _row_stride(out)
+        _check(lib.moe_grouped_gemm(ctypes.byref(a), s), "moe_grouped_gemm")
+    return out
+
+
+def moe_combine(y: torch.Tensor, w: torch.Tensor, shared: Optional[torch.Tensor] = None,
+                residual: Optional[torch.Tensor] = None, stream=None,
+                out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """y bfloat16 or float32 [M k][H], w float32 [M][k] (+ shared [M][H] of y's
+    type, residual bfloat16 [M][H]) -> bfloat16 [M][H]."""
+    if y.dim() != 2 or w.dim() != 2:
+        raise ValueError("need y [M k][H] and w [M][k]")
+    yt = _float_type(y.dtype, "y")
+    M, k = w.shape
+    H = y.shape[1]
+    dev = y.device
+    _want(y, "y", (M * k, H), y.dtype, dev)
+    _want(w, "w", (M, k), torch.float32, dev)
+    _want(shared, "shared", (M, H), y.dtype, dev)
+    _want(residual, "residual", (M, H), torch.bfloat16, dev)
+    with _On(y, stream) as s:
+        if out is None:
+            out = torch.empty((M, H), dtype=torch.bfloat16, device=dev)
+        _want(out, "out", (M, H), torch.bfloat16, dev)
+        _check(lib.moe_combine(_ptr(y), yt, _ptr(w), _ptr(shared), _ptr(residual), M, k, H,
+                               _ptr(out), s), "moe_combine")
+    return out

@@ -10,6 +10,9 @@
 
 #include "nvfp4moe.h"
 
+#include "block8.hpp"
+#include "blockgemm.hpp"
+#include "combine.hpp"
 #include "fp8.hpp"
 #include "fused.hpp"
 #include "gemm.hpp"
@@ -711,6 +714,280 @@ int32_t moe_nvfp4_route_decode_static(const moe_nvfp4_args* a, const float* logi
   const int32_t st = scratch_address(&ptr);
   if (st != NVFP4MOE_OK) return st;
   return route_decode(a, logits, bias, stream, ptr, kScratchBytes);
+}
+
+}  // extern "C"
+
+// ---- FP8 with block scales, products grouped by expert, combine -------------------------
+
+namespace {
+
+constexpr int64_t kBlockMaxRows = (int64_t)1 << 24;
+constexpr int64_t kBlockMaxN = (int64_t)1 << 20;
+constexpr int64_t kGroupedMaxE = 1024;
+constexpr int64_t kMaxGrid = ((int64_t)1 << 31) - 1;
+constexpr int64_t kBlockMaxOut = (int64_t)1 << 38;  // elements of y
+
+int32_t check_block_nk(int64_t N, int64_t K) {
+  if (N < 1 || K < 1) return fail(NVFP4MOE_ERR_BAD_SHAPE, "N and K must be >= 1");
+  if (K < 16 || K > kMaxK || K % 16 != 0)
+    return fail(NVFP4MOE_ERR_UNSUPPORTED, "K = %lld: need a multiple of 16 in [16, %lld]",
+                (long long)K, (long long)kMaxK);
+  if (N > kBlockMaxN)
+    return fail(NVFP4MOE_ERR_UNSUPPORTED, "N = %lld > %lld", (long long)N, (long long)kBlockMaxN);
+  return ok();
+}
+
+int32_t check_float_type(int32_t type, const char* what) {
+  if (type != NVFP4MOE_BF16 && type != NVFP4MOE_F32)
+    return fail(NVFP4MOE_ERR_BAD_SHAPE, "%s must be NVFP4MOE_BF16 or NVFP4MOE_F32 (got %d)", what,
+                (int)type);
+  return ok();
+}
+
+int64_t type_bytes(int32_t type) { return type == NVFP4MOE_F32 ? 4 : 2; }
+
+template <typename T>
+void launch_quantize_rows(const void* x, int64_t M, int64_t K, int64_t ldx, bool swiglu,
+                          uint8_t* codes, float* scales, hipStream_t s) {
+  const int64_t KB = blocks128(K);
+  const dim3 grid((unsigned)((M * KB + 15) / 16)), block(kQuantRowsThreads);
+  if (swiglu)
+    hipLaunchKernelGGL((fp8_quantize_rows_kernel<T, true>), grid, block, 0, s, (const T*)x, M,
+                       (int)K, ldx, (int)KB, codes, scales);
+  else
+    hipLaunchKernelGGL((fp8_quantize_rows_kernel<T, false>), grid, block, 0, s, (const T*)x, M,
+                       (int)K, ldx, (int)KB, codes, scales);
+}
+
+template <Mma MODE, bool GROUPED, int NT, int MT, int U, typename Y>
+int32_t launch_direct(const BlockGemmParams& p, const char* what, hipStream_t s) {
+  constexpr int BN = 16 * NT, BM = 16 * MT;
+  const int64_t n_tiles = (p.N + BN - 1) / BN;
+  // grouped: the most tiles that R rows in p.slots groups can take
+  const int64_t m_tiles =
+      GROUPED ? (p.R + (int64_t)p.slots * (BM - 1)) / BM : ((int64_t)p.R + BM - 1) / BM;
+  if (n_tiles * m_tiles > kMaxGrid) return fail(NVFP4MOE_ERR_UNSUPPORTED, "%s: grid too large", what);
+  hipLaunchKernelGGL((direct_gemm_kernel<MODE, GROUPED, NT, MT, U, Y>),
+                     dim3((unsigned)(n_tiles * m_tiles)), dim3(kDirectWaves * 64), 0, s, p,
+                     (int)n_tiles);
+  return launched(what);
+}
+
+template <bool FP8, bool GROUPED, typename Y>
+int32_t launch_block_gemm(const BlockGemmParams& p, const char* what, hipStream_t s) {
+  constexpr Mma kExact = FP8 ? Mma::kFp8Exact : Mma::kBf16;
+  return launch_direct<kExact, GROUPED, 1, 1, 4, Y>(p, what, s);
+}
+
+}  // namespace
+
+extern "C" {
+
+int32_t fp8_quantize_rows(const void* x, int32_t x_type, int64_t M, int64_t K, int64_t ldx,
+                          int32_t swiglu, uint8_t* codes, float* scales, hipStream_t stream) {
+  int32_t st = check_float_type(x_type, "x_type");
+  if (st != NVFP4MOE_OK) return st;
+  if (swiglu != 0 && swiglu != 1)
+    return fail(NVFP4MOE_ERR_BAD_SHAPE, "swiglu must be 0 or 1 (got %d)", (int)swiglu);
+  if (M < 0) return fail(NVFP4MOE_ERR_BAD_SHAPE, "M must be >= 0");
+  if ((st = check_block_nk(1, K)) != NVFP4MOE_OK) return st;
+  if (M > kBlockMaxRows) return fail(NVFP4MOE_ERR_UNSUPPORTED, "M = %lld too large", (long long)M);
+  const int64_t cols = swiglu ? 2 * K : K;
+  if (ldx < cols || ldx > (int64_t)1 << 32)
+    return fail(NVFP4MOE_ERR_BAD_SHAPE, "ldx = %lld: a row has %lld columns", (long long)ldx,
+                (long long)cols);
+  if (M == 0) return ok();
+  if (!x || !codes || !scales) return fail(NVFP4MOE_ERR_NULL_ARG, "fp8_quantize_rows: null");
+  if (!aligned(x, 16) || (ldx * type_bytes(x_type)) % 16 != 0 || !aligned(codes, 16) ||
+      !aligned(scales, 4))
+    return fail(NVFP4MOE_ERR_UNSUPPORTED,
+                "rows of x and codes need 16-byte, scales 4-byte alignment");
+  if (x_type == NVFP4MOE_BF16)
+    launch_quantize_rows<uint16_t>(x, M, K, ldx, swiglu != 0, codes, scales, stream);
+  else
+    launch_quantize_rows<float>(x, M, K, ldx, swiglu != 0, codes, scales, stream);
+  return launched("fp8_quantize_rows");
+}
+
+int32_t fp8_quantize_blocks(const void* x, int32_t x_type, int64_t G, int64_t N, int64_t K,
+                            uint8_t* codes, float* scales, hipStream_t stream) {
+  int32_t st = check_float_type(x_type, "x_type");
+  if (st != NVFP4MOE_OK) return st;
+  if (G < 0) return fail(NVFP4MOE_ERR_BAD_SHAPE, "G must be >= 0");
+  if ((st = check_block_nk(N, K)) != NVFP4MOE_OK) return st;
+  const int64_t NB = blocks128(N), KB = blocks128(K);
+  if (G > kMaxG || G * NB * KB > kMaxGrid)
+    return fail(NVFP4MOE_ERR_UNSUPPORTED, "G = %lld: more than 2^31 - 1 blocks", (long long)G);
+  if (G == 0) return ok();
+  if (!x || !codes || !scales) return fail(NVFP4MOE_ERR_NULL_ARG, "fp8_quantize_blocks: null");
+  if (!aligned(x, 16) || !aligned(codes, 16) || !aligned(scales, 4))
+    return fail(NVFP4MOE_ERR_UNSUPPORTED, "x and codes need 16-byte, scales 4-byte alignment");
+  const dim3 grid((unsigned)(G * NB * KB)), block(kQuantBlocksThreads);
+  if (x_type == NVFP4MOE_BF16)
+    hipLaunchKernelGGL(fp8_quantize_blocks_kernel<uint16_t>, grid, block, 0, stream,
+                       (const uint16_t*)x, N, (int)K, (int)NB, (int)KB, codes, scales);
+  else
+    hipLaunchKernelGGL(fp8_quantize_blocks_kernel<float>, grid, block, 0, stream, (const float*)x,
+                       N, (int)K, (int)NB, (int)KB, codes, scales);
+  return launched("fp8_quantize_blocks");
+}
+
+int32_t fp8_block_gemm(const uint8_t* x, const float* x_scales, int64_t M, int64_t K,
+                       const uint8_t* w, const float* w_scales, int64_t N, void* y, int32_t y_type,
+                       int64_t ldy, hipStream_t stream) {
+  int32_t st = check_float_type(y_type, "y_type");
+  if (st != NVFP4MOE_OK) return st;
+  if (M < 0) return fail(NVFP4MOE_ERR_BAD_SHAPE, "M must be >= 0");
+  if ((st = check_block_nk(N, K)) != NVFP4MOE_OK) return st;
+  if (M > kBlockMaxRows || M * N > kBlockMaxOut)
+    return fail(NVFP4MOE_ERR_UNSUPPORTED, "M = %lld too large", (long long)M);
+  if (ldy < N || ldy > (int64_t)1 << 32)
+    return fail(NVFP4MOE_ERR_BAD_SHAPE, "ldy = %lld < N = %lld", (long long)ldy, (long long)N);
+  if (M == 0) return ok();
+  if (!x || !x_scales || !w || !w_scales || !y)
+    return fail(NVFP4MOE_ERR_NULL_ARG, "fp8_block_gemm: null");
+  if (!aligned(x, 16) || !aligned(w, 16) || !aligned(x_scales, 4) || !aligned(w_scales, 4) ||
+      !aligned(y, (uintptr_t)type_bytes(y_type)))
+    return fail(NVFP4MOE_ERR_UNSUPPORTED,
+                "codes need 16-byte, scales 4-byte, y its element's alignment");
+  BlockGemmParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.x = x;
+  p.xs = x_scales;
+  p.w = w;
+  p.ws = w_scales;
+  p.y = y;
+  p.ldy = ldy;
+  p.Mx = M;
+  p.w_mat_bytes = 0;
+  p.R = (int)M;
+  p.div = 1;
+  p.slots = 1;
+  p.E = 1;
+  p.N = (int)N;
+  p.NB = (int)blocks128(N);
+  p.KB = (int)blocks128(K);
+  p.row_bytes = (int)K;
+  return y_type == NVFP4MOE_BF16
+             ? launch_block_gemm<true, false, uint16_t>(p, "fp8_block_gemm", stream)
+             : launch_block_gemm<true, false, float>(p, "fp8_block_gemm", stream);
+}
+
+int32_t moe_grouped_gemm(const moe_grouped_args* a, hipStream_t stream) {
+  if (!a) return fail(NVFP4MOE_ERR_NULL_ARG, "moe_grouped_gemm: args is null");
+  int32_t st = check_float_type(a->y_type, "y_type");
+  if (st != NVFP4MOE_OK) return st;
+  if (a->type != NVFP4MOE_BF16 && a->type != NVFP4MOE_FP8)
+    return fail(NVFP4MOE_ERR_BAD_SHAPE, "type must be NVFP4MOE_BF16 or NVFP4MOE_FP8 (got %d)",
+                (int)a->type);
+  const bool fp8 = a->type == NVFP4MOE_FP8;
+  if (a->R < 0 || a->x_rows < 0 || a->pairs_per_row < 1 || a->E < 1)
+    return fail(NVFP4MOE_ERR_BAD_SHAPE, "need R, x_rows >= 0 and pairs_per_row, E >= 1");
+  if ((st = check_block_nk(a->N, a->K)) != NVFP4MOE_OK) return st;
+  if (a->E > kGroupedMaxE || a->R >= kBlockMaxRows || a->x_rows > kBlockMaxRows ||
+      a->pairs_per_row > kBlockMaxRows || a->R * a->N > kBlockMaxOut)
+    return fail(NVFP4MOE_ERR_UNSUPPORTED,
+                "need E <= 1024, R < 2^24, x_rows <= 2^24 and R * N <= 2^38");
+  if (a->x_rows * a->pairs_per_row < a->R)
+    return fail(NVFP4MOE_ERR_BAD_SHAPE, "x_rows * pairs_per_row = %lld < R = %lld",
+                (long long)(a->x_rows * a->pairs_per_row), (long long)a->R);
+  if (a->ldy < a->N || a->ldy > (int64_t)1 << 32)
+    return fail(NVFP4MOE_ERR_BAD_SHAPE, "ldy = %lld < N = %lld", (long long)a->ldy,
+                (long long)a->N);
+  if (a->R == 0) return ok();
+  if (!a->x || !a->w || !a->pairs || !a->active || !a->active_offsets || !a->n_active || !a->y ||
+      (fp8 && (!a->x_scales || !a->w_scales)))
+    return fail(NVFP4MOE_ERR_NULL_ARG, "moe_grouped_gemm: a required pointer is null");
+  if (!aligned(a->x, 16) || !aligned(a->w, 16) ||
+      (fp8 && (!aligned(a->x_scales, 4) || !aligned(a->w_scales, 4))) || !aligned(a->pairs, 4) ||
+      !aligned(a->active, 4) || !aligned(a->active_offsets, 4) || !aligned(a->n_active, 4) ||
+      !aligned(a->y, (uintptr_t)type_bytes(a->y_type)))
+    return fail(NVFP4MOE_ERR_UNSUPPORTED,
+                "x and w need 16-byte, every other array its element's alignment");
+  BlockGemmParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.x = (const uint8_t*)a->x;
+  p.xs = a->x_scales;
+  p.w = (const uint8_t*)a->w;
+  p.ws = a->w_scales;
+  p.y = a->y;
+  p.pairs = a->pairs;
+  p.active = a->active;
+  p.active_offsets = a->active_offsets;
+  p.n_active = a->n_active;
+  p.ldy = a->ldy;
+  p.Mx = a->x_rows;
+  p.row_bytes = (int)(fp8 ? a->K : 2 * a->K);
+  p.w_mat_bytes = a->N * p.row_bytes;
+  p.R = (int)a->R;
+  p.div = (int)a->pairs_per_row;
+  p.slots = (int)(a->E < a->R ? a->E : a->R);
+  p.E = (int)a->E;
+  p.N = (int)a->N;
+  p.NB = (int)blocks128(a->N);
+  p.KB = (p.row_bytes + kStepBytes - 1) / kStepBytes;
+  const char* what = "moe_grouped_gemm";
+  if (fp8)
+    return a->y_type == NVFP4MOE_BF16 ? launch_block_gemm<true, true, uint16_t>(p, what, stream)
+                                      : launch_block_gemm<true, true, float>(p, what, stream);
+  return a->y_type == NVFP4MOE_BF16 ? launch_block_gemm<false, true, uint16_t>(p, what, stream)
+                                    : launch_block_gemm<false, true, float>(p, what, stream);
+}
+
+}  // extern "C"
+
+namespace {
+
+template <typename T, int V>
+void launch_moe_combine(const T* y, const float* w, const T* shared, const uint16_t* residual,
+                        int64_t M, int64_t k, int64_t H, uint16_t* out, hipStream_t s) {
+  const int64_t per_row = H / V, units = M * per_row;
+  hipLaunchKernelGGL((combine_kernel<T, V, 8>),
+                     dim3((unsigned)((units + kCombineThreads - 1) / kCombineThreads)),
+                     dim3(kCombineThreads), 0, s, y, w, shared, residual, units, (int)per_row,
+                     (int)k, H, out);
+}
+
+template <typename T>
+int32_t combine_typed(const void* y, const float* w, const void* shared, const uint16_t* residual,
+                      int64_t M, int64_t k, int64_t H, uint16_t* out, hipStream_t s) {
+  const T* yt = (const T*)y;
+  const T* st = (const T*)shared;
+  // four outputs a thread where every row of every array is aligned for it
+  const bool vec = H % 4 == 0 && aligned(y, 4 * sizeof(T)) && aligned(shared, 4 * sizeof(T)) &&
+                   aligned(residual, 8) && aligned(out, 8);
+  if (vec)
+    launch_moe_combine<T, 4>(yt, w, st, residual, M, k, H, out, s);
+  else
+    launch_moe_combine<T, 1>(yt, w, st, residual, M, k, H, out, s);
+  return launched("moe_combine");
+}
+
+}  // namespace
+
+extern "C" {
+
+int32_t moe_combine(const void* y, int32_t y_type, const float* w, const void* shared,
+                    const uint16_t* residual, int64_t M, int64_t k, int64_t H, uint16_t* out,
+                    hipStream_t stream) {
+  int32_t st = check_float_type(y_type, "y_type");
+  if (st != NVFP4MOE_OK) return st;
+  if (M < 0 || k < 1 || H < 1)
+    return fail(NVFP4MOE_ERR_BAD_SHAPE, "need M >= 0 and k, H >= 1");
+  if (k > kRouteMaxK || M > kBlockMaxRows || H > kBlockMaxN)
+    return fail(NVFP4MOE_ERR_UNSUPPORTED, "need k <= 8, M <= 2^24 and H <= 2^20");
+  if ((M * H + kCombineThreads - 1) / kCombineThreads > kMaxGrid)
+    return fail(NVFP4MOE_ERR_UNSUPPORTED, "moe_combine: grid too large");
+  if (M == 0) return ok();
+  if (!y || !w || !out) return fail(NVFP4MOE_ERR_NULL_ARG, "moe_combine: null");
+  const uintptr_t el = (uintptr_t)type_bytes(y_type);
+  if (!aligned(y, el) || !aligned(w, 4) || !aligned(shared, el) || !aligned(residual, 2) ||
+      !aligned(out, 2))
+    return fail(NVFP4MOE_ERR_UNSUPPORTED, "moe_combine: an array is not aligned to its element");
+  return y_type == NVFP4MOE_BF16
+             ? combine_typed<uint16_t>(y, w, shared, residual, M, k, H, out, stream)
+             : combine_typed<float>(y, w, shared, residual, M, k, H, out, stream);
 }
 
 }  // extern "C"
