@@ -760,24 +760,74 @@ void launch_quantize_rows(const void* x, int64_t M, int64_t K, int64_t ldx, bool
                        (int)K, ldx, (int)KB, codes, scales);
 }
 
-template <Mma MODE, bool GROUPED, int NT, int MT, int U, typename Y>
-int32_t launch_direct(const BlockGemmParams& p, const char* what, hipStream_t s) {
-  constexpr int BN = 16 * NT, BM = 16 * MT;
+// Blocks of BM x BN tiles, a multiple of eight (one part per XCD); grouped: of
+// the most row tiles that R rows in p.slots groups can take. < 0: too many.
+int64_t block_gemm_grid(const BlockGemmParams& p, bool grouped, int BN, int BM) {
   const int64_t n_tiles = (p.N + BN - 1) / BN;
-  // grouped: the most tiles that R rows in p.slots groups can take
-  const int64_t m_tiles =
-      GROUPED ? (p.R + (int64_t)p.slots * (BM - 1)) / BM : ((int64_t)p.R + BM - 1) / BM;
-  if (n_tiles * m_tiles > kMaxGrid) return fail(NVFP4MOE_ERR_UNSUPPORTED, "%s: grid too large", what);
-  hipLaunchKernelGGL((direct_gemm_kernel<MODE, GROUPED, NT, MT, U, Y>),
-                     dim3((unsigned)(n_tiles * m_tiles)), dim3(kDirectWaves * 64), 0, s, p,
-                     (int)n_tiles);
+  const int64_t rows = (int64_t)p.R + (grouped ? (int64_t)p.slots : 1) * (BM - 1);
+  const int64_t blocks = (n_tiles * (rows / BM) + 7) / 8 * 8;
+  return blocks > kMaxGrid ? -1 : blocks;
+}
+
+int32_t grid_too_large(const char* what) {
+  return fail(NVFP4MOE_ERR_UNSUPPORTED, "%s: more tiles than a grid holds", what);
+}
+
+template <Mma MODE, bool GROUPED, typename Y>
+int32_t launch_direct(const BlockGemmParams& p, const char* what, hipStream_t s) {
+  constexpr int NT = 1, MT = 1, U = 4;
+  const int64_t grid = block_gemm_grid(p, GROUPED, 16 * NT, 16 * MT);
+  if (grid < 0) return grid_too_large(what);
+  hipLaunchKernelGGL((direct_gemm_kernel<MODE, GROUPED, NT, MT, U, Y>), dim3((unsigned)grid),
+                     dim3(kDirectWaves * 64), 0, s, p, (p.N + 16 * NT - 1) / (16 * NT));
   return launched(what);
 }
 
+template <Mma MODE, bool GROUPED, int BN, int BM, int WVN, int WVM, int S, typename Y>
+int32_t launch_tiled(const BlockGemmParams& p, const char* what, hipStream_t s) {
+  const int64_t grid = block_gemm_grid(p, GROUPED, BN, BM);
+  if (grid < 0) return grid_too_large(what);
+  hipLaunchKernelGGL((tiled_gemm_kernel<MODE, GROUPED, BN, BM, WVN, WVM, S, Y>),
+                     dim3((unsigned)grid), dim3(WVN * WVM * 64), 0, s, p, (p.N + BN - 1) / BN);
+  return launched(what);
+}
+
+int64_t tiles_of(int64_t n, int64_t per) { return (n + per - 1) / per; }
+
+// Which kernel and tile: few blocks need many short ones to fill the chip,
+// many rows need large tiles (fewer bytes through L2 per product). The
+// thresholds are crossovers measured on an MI355X (us, FP8 -> BF16 unless
+// noted; weights cycled through more than the Infinity Cache):
+//   dense    N = 5120, K = 2048
+//     M = 1         direct 5.5, 128x32 tiles 11 (FP32 result)
+//     M = 32        direct 8.8 (640 blocks), 64x64 8.1;  M = 64: 13, 7.6
+//     M = 24, N = 1000, K = 4096   direct 6.7 (126 blocks), 64x64 19 (FP32 result)
+//     M = 512       64x64 13.6 (640 blocks), 128x64 13.4;  M = 2048: 45, 37
+//     M = 2048      128x64 37.4 (1280 blocks), 256x128 39.5;  M = 8192: 131, 107
+//   grouped  E = 256, k = 8, gate_up 2048 -> 1024
+//     M = 1         direct 6.0, 128x32 12.7 (FP32 result);  M = 4: 16.8, 14.0
+//     M = 256       128x32 96 (8 rows a slot), 128x64 98;  M = 1024 (32): 121, 108
+//     M = 1024      128x64 108, 256x128 119;  M = 512, E = 64 (64): 42, 33
+//     M = 256, E = 8, k = 2        64x64 11.2 (128 blocks), 256x128 21
 template <bool FP8, bool GROUPED, typename Y>
 int32_t launch_block_gemm(const BlockGemmParams& p, const char* what, hipStream_t s) {
   constexpr Mma kExact = FP8 ? Mma::kFp8Exact : Mma::kBf16;
-  return launch_direct<kExact, GROUPED, 1, 1, 4, Y>(p, what, s);
+  constexpr Mma kFast = FP8 && sizeof(Y) == 2 ? Mma::kFp8 : kExact;
+  const int64_t per_slot = tiles_of(p.R, p.slots);  // mean rows of a slot (dense: all)
+  const int64_t direct = p.slots * tiles_of(per_slot, 16) * tiles_of(p.N, 16);
+  const int64_t small = p.slots * tiles_of(per_slot, 64) * tiles_of(p.N, 64);
+  if constexpr (GROUPED) {
+    if (per_slot <= 8 && direct <= 1024) return launch_direct<kExact, GROUPED, Y>(p, what, s);
+    if (per_slot <= 16) return launch_tiled<kFast, GROUPED, 128, 32, 4, 1, 3, Y>(p, what, s);
+    if (small <= 640) return launch_tiled<kFast, GROUPED, 64, 64, 2, 2, 3, Y>(p, what, s);
+    if (per_slot < 48) return launch_tiled<kFast, GROUPED, 128, 64, 2, 2, 3, Y>(p, what, s);
+  } else {
+    if (direct <= 640) return launch_direct<kExact, GROUPED, Y>(p, what, s);
+    if (p.R <= 32) return launch_tiled<kFast, GROUPED, 128, 32, 4, 1, 3, Y>(p, what, s);
+    if (small <= 640) return launch_tiled<kFast, GROUPED, 64, 64, 2, 2, 3, Y>(p, what, s);
+    if (small <= 2560) return launch_tiled<kFast, GROUPED, 128, 64, 2, 2, 3, Y>(p, what, s);
+  }
+  return launch_tiled<kFast, GROUPED, 256, 128, 4, 2, 3, Y>(p, what, s);
 }
 
 }  // namespace

@@ -71,6 +71,19 @@ struct Frag {
   uint4 lo, hi;
 };
 
+__device__ __forceinline__ void keep(uint4& v, uint32_t mask) {
+  v.x &= mask;
+  v.y &= mask;
+  v.z &= mask;
+  v.w &= mask;
+}
+
+// Zeroes the pieces whose mask is 0 (those past K in the last step).
+__device__ __forceinline__ void mask_frag(Frag& f, uint32_t lo, uint32_t hi) {
+  keep(f.lo, lo);
+  keep(f.hi, hi);
+}
+
 enum class Mma {
   kBf16,      // BF16 operands
   kFp8Exact,  // E4M3 codes decoded to BF16
@@ -113,6 +126,26 @@ struct Operand<Mma::kFp8> {
   }
 };
 
+// The sum over one scale block.
+template <Mma MODE>
+__device__ __forceinline__ bg_f32x4 block_mma(const Operand<MODE>& a, const Operand<MODE>& b) {
+  bg_f32x4 t = {0.0f, 0.0f, 0.0f, 0.0f};
+  if constexpr (MODE == Mma::kFp8) {
+    t = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a.v, b.v, t, 0, 0, 0, 0, 0,
+                                                         0);  // E4M3 x E4M3, no scale operand
+  } else {
+#pragma unroll
+    for (int i = 0; i < (int)(sizeof(a.v) / sizeof(a.v[0])); ++i)
+      t = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.v[i], b.v[i], t, 0, 0, 0);
+  }
+  return t;
+}
+
+__device__ __forceinline__ void scale_into(const bg_f32x4& t, float s, bg_f32x4& acc) {
+#pragma unroll
+  for (int r = 0; r < 4; ++r) acc[r] = fmaf(t[r], s, acc[r]);
+}
+
 // acc += (A B) * s over one k step (BF16 operands: s is 1 and not applied).
 template <Mma MODE>
 __device__ __forceinline__ void step_mma(const Operand<MODE>& a, const Operand<MODE>& b, float s,
@@ -122,17 +155,7 @@ __device__ __forceinline__ void step_mma(const Operand<MODE>& a, const Operand<M
     for (int i = 0; i < 2; ++i)
       acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.v[i], b.v[i], acc, 0, 0, 0);
   } else {
-    bg_f32x4 t = {0.0f, 0.0f, 0.0f, 0.0f};
-    if constexpr (MODE == Mma::kFp8) {
-      t = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a.v, b.v, t, 0, 0, 0, 0, 0,
-                                                           0);  // E4M3 x E4M3, no scale operand
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        t = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.v[i], b.v[i], t, 0, 0, 0);
-    }
-#pragma unroll
-    for (int r = 0; r < 4; ++r) acc[r] = fmaf(t[r], s, acc[r]);
+    scale_into(block_mma<MODE>(a, b), s, acc);
   }
 }
 
@@ -179,13 +202,27 @@ __device__ __forceinline__ int wave_inclusive_sum(int v, int lane) {
   return v;
 }
 
-// Row tile t of the slots' tiles in slot order (t uniform; the whole wave active).
+// Tiles of BM rows in all slots (the whole wave active); first: the slots 0 .. 255.
 template <int BM>
-__device__ __forceinline__ RowTile find_tile(const BlockGemmParams& p, int t, int lane) {
-  RowTile r = {0, 0, 0};
-  for (int base = 0; base < p.slots; base += 256) {
+__device__ __forceinline__ int count_tiles(const BlockGemmParams& p, const SlotTiles<BM>& first,
+                                           int lane) {
+  int total = __builtin_amdgcn_readlane(wave_inclusive_sum(first.sum, lane), 63);
+  for (int base = 256; base < p.slots; base += 256) {
     SlotTiles<BM> st;
     st.load(p, base, lane);
+    total += __builtin_amdgcn_readlane(wave_inclusive_sum(st.sum, lane), 63);
+  }
+  return total;
+}
+
+// Row tile t of the slots' tiles in slot order (t uniform; the whole wave active).
+template <int BM>
+__device__ __forceinline__ RowTile find_tile(const BlockGemmParams& p, const SlotTiles<BM>& first,
+                                             int t, int lane) {
+  RowTile r = {0, 0, 0};
+  for (int base = 0; base < p.slots; base += 256) {
+    SlotTiles<BM> st = first;
+    if (base > 0) st.load(p, base, lane);
     const int incl = wave_inclusive_sum(st.sum, lane);
     const int total = __builtin_amdgcn_readlane(incl, 63);
     if (t < total) {
@@ -212,14 +249,48 @@ __device__ __forceinline__ RowTile find_tile(const BlockGemmParams& p, int t, in
   return r;
 }
 
-template <int BM, bool GROUPED>
-__device__ __forceinline__ RowTile row_tile(const BlockGemmParams& p, int t, int lane) {
+// A block's work: a row tile and the first of its weight rows.
+struct Work {
+  RowTile t;
+  int n0;
+};
+
+// Blocks are handed to the eight XCDs in turn (block b to XCD b % 8), each with
+// its own L2, so XCD x gets the consecutive part [x T / 8, (x + 1) T / 8) of
+// the T tiles, in bands of eight row tiles: within a band all row tiles of one
+// column of weight rows, then the next column. The blocks an XCD runs at a time
+// then share row tiles and weight rows about equally, and an expert's weights
+// stay on one XCD or two. The grid has 8 ceil(Tmax / 8) blocks; those past
+// their XCD's part have no rows.
+template <int BN, int BM, bool GROUPED>
+__device__ __forceinline__ Work block_work(const BlockGemmParams& p, int n_tiles, int lane) {
+  constexpr int kBand = 8;
+  SlotTiles<BM> first;
+  int m_tiles;
   if constexpr (GROUPED) {
-    return find_tile<BM>(p, t, lane);
+    first.load(p, 0, lane);
+    m_tiles = count_tiles<BM>(p, first, lane);
   } else {
-    const int row0 = t * BM;
-    return {0, row0, min(p.R - row0, BM)};
+    m_tiles = (p.R + BM - 1) / BM;
   }
+  Work w = {{0, 0, 0}, 0};
+  const uint32_t tiles = (uint32_t)m_tiles * (uint32_t)n_tiles;  // at most the grid, < 2^31
+  const uint32_t x = blockIdx.x & 7, i = blockIdx.x >> 3;
+  const uint32_t q0 = tiles / 8 * x + tiles % 8 * x / 8;
+  const uint32_t q1 = tiles / 8 * (x + 1) + tiles % 8 * (x + 1) / 8;
+  const uint32_t q = q0 + i;
+  if (q >= q1) return w;
+  const uint32_t per_band = kBand * (uint32_t)n_tiles;
+  const uint32_t band = q / per_band, in = q - band * per_band;
+  const uint32_t rows = min((uint32_t)kBand, (uint32_t)m_tiles - band * kBand);
+  const uint32_t n = in / rows;
+  const int m = (int)(band * kBand + (in - n * rows));
+  w.n0 = (int)n * BN;
+  if constexpr (GROUPED)
+    w.t = find_tile<BM>(p, first, m, lane);
+  else
+    w.t = {0, m * BM, min(p.R - m * BM, BM)};
+  return w;
 }
 
 // y row of row i of a tile; -1 for rows past the tile's last or a pair index
@@ -258,9 +329,9 @@ __global__ void __launch_bounds__(kDirectWaves * 64) direct_gemm_kernel(BlockGem
   __shared__ float red[W][BM][BN + 1];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int tile = (int)(blockIdx.x / (unsigned)n_tiles);
-  const int n0 = (int)(blockIdx.x % (unsigned)n_tiles) * BN;
-  const RowTile t = row_tile<BM, GROUPED>(p, tile, lane);
+  const Work work = block_work<BN, BM, GROUPED>(p, n_tiles, lane);
+  const RowTile t = work.t;
+  const int n0 = work.n0;
   if (t.rows <= 0) return;
   const int c = lane & 15, g = lane >> 4;
 
@@ -315,18 +386,12 @@ __global__ void __launch_bounds__(kDirectWaves * 64) direct_gemm_kernel(BlockGem
       if (kb >= p.KB) break;
       const int base = kb * kStepBytes;
       if (base + kStepBytes > p.row_bytes) {  // the last step, partly past K
-        const uint4 z = make_uint4(0, 0, 0, 0);
-        const bool k0 = base + 16 * g < p.row_bytes, k1 = base + 64 + 16 * g < p.row_bytes;
+        const uint32_t k0 = base + 16 * g < p.row_bytes ? ~0u : 0u;
+        const uint32_t k1 = base + 64 + 16 * g < p.row_bytes ? ~0u : 0u;
 #pragma unroll
-        for (int i = 0; i < NT; ++i) {
-          a[u][i].lo = k0 ? a[u][i].lo : z;
-          a[u][i].hi = k1 ? a[u][i].hi : z;
-        }
+        for (int i = 0; i < NT; ++i) mask_frag(a[u][i], k0, k1);
 #pragma unroll
-        for (int j = 0; j < MT; ++j) {
-          b[u][j].lo = k0 ? b[u][j].lo : z;
-          b[u][j].hi = k1 ? b[u][j].hi : z;
-        }
+        for (int j = 0; j < MT; ++j) mask_frag(b[u][j], k0, k1);
       }
       Operand<MODE> ao[NT];
 #pragma unroll
@@ -355,6 +420,348 @@ __global__ void __launch_bounds__(kDirectWaves * 64) direct_gemm_kernel(BlockGem
     for (int q = 1; q < W; ++q) v += red[q][m][n];
     const int yr = y_row<GROUPED>(p, t, m);
     if (yr >= 0 && n0 + n < p.N) store_y(static_cast<Y*>(p.y) + yr * p.ldy + n0 + n, v);
+  }
+}
+
+// ---- many rows: operands staged in LDS --------------------------------------------------
+//
+// One block per (row tile of BM rows, BN weight rows), wave tiles of
+// BN / WVN x BM / WVM. A k step of the BN + BM rows (128 bytes each, and the x
+// scales) is copied to LDS by direct loads; with S stages, S - 1 steps are in
+// flight or ready while one is multiplied.
+// Piece c of row r lies at piece c ^ (r % 8) of the row's 128 bytes, so lanes
+// that read the same piece of neighbouring rows hit different banks (no bank
+// conflict counted in the loop); the copy's lanes are contiguous in LDS, so
+// the exchange is made on the global side (eight lanes still read one row's
+// whole 128 bytes).
+typedef __attribute__((address_space(3))) void lds_void;
+typedef const __attribute__((address_space(1))) void global_void;
+
+// The lane's 16 (4) bytes at src to dst + 16 (4) * lane; dst is wave-uniform.
+__device__ __forceinline__ void copy16_to_lds(const uint8_t* src, uint8_t* dst) {
+  __builtin_amdgcn_global_load_lds((global_void*)src, (lds_void*)dst, 16, 0, 0);
+}
+__device__ __forceinline__ void copy4_to_lds(const float* src, uint8_t* dst) {
+  __builtin_amdgcn_global_load_lds((global_void*)src, (lds_void*)dst, 4, 0, 0);
+}
+
+// Waits until at most N of the wave's vector memory requests are outstanding.
+template <int N>
+__device__ __forceinline__ void wait_vmem() {
+  static_assert(N >= 0 && N < 64, "");
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+
+template <Mma MODE, bool GROUPED, int BN, int BM, int WVN, int WVM, int S, typename Y>
+struct Tiled {
+  static constexpr bool FP8 = MODE != Mma::kBf16;
+  static constexpr int kWaves = WVN * WVM, kThreads = kWaves * 64;
+  static constexpr int WN = BN / WVN, WM = BM / WVM, NT = WN / 16, MT = WM / 16;
+  // copies per wave and step: weight rows, x rows, x scales of the wave's rows
+  static constexpr int LA = BN / 8 / kWaves, LB = BM / 8 / kWaves;
+  static constexpr int LS = FP8 ? (WM + 63) / 64 : 0;
+  static constexpr int kCopies = LA + LB + LS;
+  static constexpr int kScales = (BN + BM) * kStepBytes;  // where a stage's scales start
+  static constexpr int kStageBytes = kScales + kWaves * LS * 256;
+  static_assert(LA * 8 * kWaves == BN && LB * 8 * kWaves == BM, "rows split evenly over the waves");
+  static_assert(kBlock8 % WN == 0, "a wave's weight rows share a scale block");
+  static_assert(S * kStageBytes <= 160 * 1024, "the stages fit the LDS");
+
+  // What a lane copies: byte offsets of its rows (weights: from the tile's
+  // first row; x: from the tile's first row, or of any row when gathered),
+  // and the x rows whose scales it copies.
+  struct Rows {
+    uint32_t a[LA];
+    uint64_t b[LB];  // dense: below 2^32
+    uint32_t s[LS ? LS : 1];
+  };
+
+  // Copies a step into a stage. w, x, xs: the bases plus the step's offset.
+  // Pieces past K read the step's first piece (zeroed after the read from LDS).
+  static __device__ __forceinline__ void copy(const Rows& r, const uint8_t* w, const uint8_t* x,
+                                              const float* xs, int base, int piece, int row_bytes,
+                                              int wave, uint8_t* stage) {
+    const uint32_t o = base + 16 * piece < row_bytes ? 16 * piece : 0;
+#pragma unroll
+    for (int j = 0; j < LA; ++j)
+      copy16_to_lds(w + (uint32_t)(r.a[j] + o), stage + (j * kWaves + wave) * 1024);
+#pragma unroll
+    for (int j = 0; j < LB; ++j)
+      copy16_to_lds(x + (GROUPED ? r.b[j] + o : (uint32_t)((uint32_t)r.b[j] + o)),
+                      stage + BN * kStepBytes + (j * kWaves + wave) * 1024);
+#pragma unroll
+    for (int j = 0; j < LS; ++j)
+      copy4_to_lds(xs + r.s[j], stage + kScales + (wave * LS + j) * 256);
+  }
+
+  // TAIL: the last step, which may end past K (k0, k1: masks of the lane's pieces).
+  template <bool TAIL>
+  static __device__ __forceinline__ Frag read(const uint8_t* rows, int row, int lo, uint32_t k0,
+                                              uint32_t k1) {
+    const uint8_t* r = rows + row * kStepBytes;
+    Frag f;
+    f.lo = *reinterpret_cast<const uint4*>(r + lo);
+    f.hi = *reinterpret_cast<const uint4*>(r + (lo ^ 64));
+    if constexpr (TAIL) mask_frag(f, k0, k1);
+    return f;
+  }
+
+  // The products of one step; ahead() requests a later step once this step's
+  // first operands are requested. FP8: a tile's block sum is scaled into the
+  // result two instructions later, while the matrix cores work on (the
+  // scheduling barriers keep that order: left alone, the compiler moves the
+  // scaling next to its product and waits there).
+  template <bool TAIL, typename Ahead>
+  static __device__ __forceinline__ void products(const uint8_t* stage, int base, int row_bytes,
+                                                  int wave, int wn, int wm, int lane, float ws,
+                                                  bg_f32x4 (&acc)[NT][MT], Ahead ahead) {
+    constexpr int kLag = NT * MT >= 2 ? 2 : 1;
+    const int c = lane & 15, g = lane >> 4;
+    const int lo = 16 * (g ^ (c & 7));
+    const uint32_t k0 = base + 16 * g < row_bytes ? ~0u : 0u;
+    const uint32_t k1 = base + 64 + 16 * g < row_bytes ? ~0u : 0u;
+    const uint8_t* wrows = stage + (wn + c) * kStepBytes;
+    const uint8_t* xrows = stage + (BN + wm + c) * kStepBytes;
+    const float* xs = reinterpret_cast<const float*>(stage + kScales + wave * LS * 256) + c;
+    Operand<MODE> b[MT], a[2];
+    float s[MT];
+    // x operands that are requested before the first product; the others
+    // follow one product behind another, so that the first ones need not wait
+    // for all of them (LDS answers in order, and every wave asks at once)
+    constexpr int kFirst = MODE == Mma::kFp8 && MT > 2 ? 2 : MT;
+    a[0].set(read<TAIL>(wrows, 0, lo, k0, k1));
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int j = 0; j < kFirst; ++j) {
+      b[j].set(read<TAIL>(xrows, 16 * j, lo, k0, k1));
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    ahead();
+    __builtin_amdgcn_sched_barrier(0);
+    if constexpr (kFirst == MT) {
+#pragma unroll
+      for (int j = 0; j < MT; ++j) s[j] = FP8 ? xs[16 * j] : 1.0f;
+    }
+    if constexpr (MODE == Mma::kFp8) {
+      bg_f32x4 t[kLag + 1];
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
+#pragma unroll
+        for (int j = 0; j < MT; ++j) {
+          const int q = i * MT + j, d = q - kLag;
+          t[q % (kLag + 1)] = block_mma<MODE>(a[i & 1], b[j]);
+          __builtin_amdgcn_sched_barrier(0);
+          if (i == 0 && j + kFirst < MT) {
+            b[j + kFirst].set(read<TAIL>(xrows, 16 * (j + kFirst), lo, k0, k1));
+            __builtin_amdgcn_sched_barrier(0);
+          }
+          if (kFirst < MT && q == 0) {
+#pragma unroll
+            for (int v = 0; v < MT; ++v) s[v] = xs[16 * v];
+            __builtin_amdgcn_sched_barrier(0);
+          }
+          if (i == 0 && kFirst == MT) s[j] *= ws;
+          if (kFirst < MT && q == 1) {
+#pragma unroll
+            for (int v = 0; v < MT; ++v) s[v] *= ws;
+          }
+          if (d >= 0) scale_into(t[d % (kLag + 1)], s[d % MT], acc[d / MT][d % MT]);
+          if (j == 0 && i + 1 < NT)
+            a[(i + 1) & 1].set(read<TAIL>(wrows, 16 * (i + 1), lo, k0, k1));
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      }
+#pragma unroll
+      for (int d = NT * MT - kLag; d < NT * MT; ++d)
+        scale_into(t[d % (kLag + 1)], s[d % MT], acc[d / MT][d % MT]);
+    } else {
+      // several instructions per tile and step: those of a row of tiles in
+      // turn, so that none waits for the one before it
+      constexpr int kParts = (int)(sizeof(a[0].v) / sizeof(a[0].v[0]));
+#pragma unroll
+      for (int j = 0; j < MT; ++j) s[j] *= ws;
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
+        bg_f32x4 t[MT];
+#pragma unroll
+        for (int j = 0; j < MT; ++j) t[j] = FP8 ? bg_f32x4{0.0f, 0.0f, 0.0f, 0.0f} : acc[i][j];
+#pragma unroll
+        for (int e = 0; e < kParts; ++e)
+#pragma unroll
+          for (int j = 0; j < MT; ++j)
+            t[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[i & 1].v[e], b[j].v[e], t[j], 0, 0, 0);
+        if (i + 1 < NT) a[(i + 1) & 1].set(read<TAIL>(wrows, 16 * (i + 1), lo, k0, k1));
+#pragma unroll
+        for (int j = 0; j < MT; ++j) {
+          if constexpr (FP8)
+            scale_into(t[j], s[j], acc[i][j]);
+          else
+            acc[i][j] = t[j];
+        }
+      }
+    }
+  }
+};
+
+__device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
+  typedef __bf16 v2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, v2{(__bf16)a, (__bf16)b});  // RNE, one instruction
+}
+
+// Four consecutive results in y's type.
+__device__ __forceinline__ void pack4(const bg_f32x4& v, uint16_t* dst) {
+  *reinterpret_cast<uint2*>(dst) = make_uint2(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]));
+}
+__device__ __forceinline__ void pack4(const bg_f32x4& v, float* dst) {
+  *reinterpret_cast<bg_f32x4*>(dst) = v;
+}
+
+template <Mma MODE, bool GROUPED, int BN, int BM, int WVN, int WVM, int S, typename Y>
+__global__ void __launch_bounds__(WVN* WVM * 64, 2)
+    tiled_gemm_kernel(BlockGemmParams p, int n_tiles) {
+  using T = Tiled<MODE, GROUPED, BN, BM, WVN, WVM, S, Y>;
+  __shared__ __align__(1024) uint8_t stages[S * T::kStageBytes];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const Work work = block_work<BN, BM, GROUPED>(p, n_tiles, lane);
+  const RowTile t = work.t;
+  const int n0 = work.n0;
+  if (t.rows <= 0) return;
+
+  const int piece = (lane & 7) ^ (lane >> 3);
+  const int wn = (wave % WVN) * T::WN, wm = (wave / WVN) * T::WM;
+  const uint8_t* wk = p.w + t.e * p.w_mat_bytes + (int64_t)n0 * p.row_bytes;
+  const uint8_t* xk = GROUPED ? p.x : p.x + (int64_t)t.row0 * p.row_bytes;
+  const float* xsk = p.xs;
+  typename T::Rows rows;
+#pragma unroll
+  for (int j = 0; j < T::LA; ++j) {
+    const int n = min((j * T::kWaves + wave) * 8 + (lane >> 3), p.N - 1 - n0);
+    rows.a[j] = (uint32_t)n * (uint32_t)p.row_bytes;
+  }
+#pragma unroll
+  for (int j = 0; j < T::LB; ++j) {
+    const int r = (j * T::kWaves + wave) * 8 + (lane >> 3);
+    if constexpr (GROUPED)
+      rows.b[j] = (uint64_t)x_row<GROUPED>(p, t, r) * (uint32_t)p.row_bytes;
+    else
+      rows.b[j] = (uint32_t)min(r, t.rows - 1) * (uint32_t)p.row_bytes;
+  }
+#pragma unroll
+  for (int j = 0; j < T::LS; ++j)
+    rows.s[j] = (uint32_t)x_row<GROUPED>(p, t, wm + 64 * j + (lane & (T::WM < 64 ? T::WM - 1 : 63)));
+  // the weight scales of 64 steps, one a lane
+  const float* wsr = nullptr;
+  float ws_lanes = 1.0f;
+  if constexpr (T::FP8) {
+    wsr = p.ws + ((int64_t)t.e * p.NB + min((n0 + wn) / kBlock8, p.NB - 1)) * p.KB;
+    ws_lanes = wsr[min(lane, p.KB - 1)];
+  }
+
+  bg_f32x4 acc[T::NT][T::MT];
+#pragma unroll
+  for (int i = 0; i < T::NT; ++i)
+#pragma unroll
+    for (int j = 0; j < T::MT; ++j) acc[i][j] = {0.0f, 0.0f, 0.0f, 0.0f};
+
+  int issued = 0;  // steps requested so far
+  auto request = [&](uint8_t* __restrict__ stage) {
+    T::copy(rows, wk, xk, xsk, issued * kStepBytes, piece, p.row_bytes, wave, stage);
+    wk += kStepBytes;
+    xk += kStepBytes;
+    if constexpr (T::FP8) xsk += p.Mx;
+    ++issued;
+  };
+#pragma unroll
+  for (int q = 0; q < S - 1; ++q)
+    if (q < p.KB) request(stages + q * T::kStageBytes);
+  // (the empty asm is a use: the wait for this load stays here and in the
+  // reload's branch, instead of one for every request in every step)
+  asm volatile("" : "+v"(ws_lanes));
+
+  // Step kb, held by cur. Of the wave's requests only those of the steps after
+  // kb may be outstanding, then the barrier makes every wave's part of cur
+  // visible; it also says that every wave is done with the stage of step
+  // kb - 1, which is the one that is filled next.
+  auto arrive = [&](int kb) {
+    if (kb + S - 2 < p.KB)
+      wait_vmem<(S - 2) * T::kCopies>();
+    else
+      wait_vmem<0>();
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  auto ws_of = [&](int kb) {
+    if (T::FP8 && kb > 0 && (kb & 63) == 0) {
+      ws_lanes = wsr[min(kb + lane, p.KB - 1)];
+      asm volatile("" : "+v"(ws_lanes));
+    }
+    return T::FP8 ? __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(ws_lanes), kb & 63))
+                  : 1.0f;
+  };
+  auto step = [&](int kb, const uint8_t* __restrict__ cur, uint8_t* __restrict__ next) {
+    T::template products<false>(cur, kb * kStepBytes, p.row_bytes, wave, wn, wm, lane, ws_of(kb),
+                                acc, [&] {
+                                  if (issued < p.KB) request(next);
+                                });
+  };
+  uint32_t at = 0, fill = (S - 1) * T::kStageBytes;
+  auto advance = [](uint32_t v) {
+    v += T::kStageBytes;
+    return v == S * T::kStageBytes ? 0u : v;
+  };
+#pragma unroll 1
+  for (int kb = 0; kb + 1 < p.KB; ++kb) {
+    arrive(kb);
+    step(kb, stages + at, stages + fill);
+    at = advance(at);
+    fill = advance(fill);
+  }
+  arrive(p.KB - 1);
+  T::template products<true>(stages + at, (p.KB - 1) * kStepBytes, p.row_bytes, wave, wn, wm, lane,
+                             ws_of(p.KB - 1), acc, [] {});
+
+  // The results, 16 token rows at a time through the wave's own LDS: a lane
+  // holds four n of one row, and the 16 rows of one store would take 32 bytes
+  // each; read back, eight or more lanes write one row's consecutive 16-byte
+  // pieces.
+  __syncthreads();  // the last step's reads
+  constexpr int kRow = T::WN * (int)sizeof(Y) + 16, kPieces = T::WN * (int)sizeof(Y) / 16;
+  constexpr int kPer = 16 / (int)sizeof(Y);  // elements of a piece
+  static_assert(T::kWaves * 16 * kRow <= S * T::kStageBytes, "the exchange fits the stages");
+  uint8_t* ex = stages + wave * 16 * kRow;
+  const bool aligned16 =
+      (p.ldy % kPer | (int64_t)((uintptr_t)p.y % 16)) == 0;  // rows of y start on 16 bytes
+#pragma unroll
+  for (int j = 0; j < T::MT; ++j) {
+    if (wm + 16 * j >= t.rows) break;
+#pragma unroll
+    for (int i = 0; i < T::NT; ++i)
+      pack4(acc[i][j], reinterpret_cast<Y*>(ex + (lane & 15) * kRow) + 16 * i + 4 * (lane >> 4));
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int q = lane; q < 16 * kPieces; q += 64) {
+      const int r = q / kPieces, piece_n = (q % kPieces) * kPer;
+      const int yr = y_row<GROUPED>(p, t, wm + 16 * j + r);
+      const uint4 v = *reinterpret_cast<const uint4*>(ex + r * kRow + (q % kPieces) * 16);
+      const int n = n0 + wn + piece_n;
+      if (yr < 0 || n >= p.N) continue;
+      Y* dst = static_cast<Y*>(p.y) + yr * p.ldy + n;
+      if (aligned16 && n + kPer <= p.N) {
+        *reinterpret_cast<uint4*>(dst) = v;
+      } else {
+        Y el[kPer];
+        __builtin_memcpy(el, &v, 16);
+#pragma unroll
+        for (int e = 0; e < kPer; ++e)
+          if (n + e < p.N) dst[e] = el[e];
+      }
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
   }
 }
 
