@@ -161,7 +161,7 @@ def _want(t: Optional[torch.Tensor], name: str, shape, dtype, device):
     shape and dtype on `device` (the kernels index it by these sizes)."""
     if t is None:
         return
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+    if t.shape != shape or t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, x on {device}")
@@ -519,34 +519,41 @@ def _blocks128(n: int) -> int:
     return (n + 127) // 128
 
 
-class _On:
-    """The device of a call's tensors and the stream it runs on (the given
-    one, or that device's current one), both current while the call allocates
-    its outputs and launches."""
+# The raw handle of a device's current stream (the plain accessor builds a
+# Stream object for it, 2.8 us against 0.1 where a small call takes 8 in all).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
 
-    def __init__(self, t: torch.Tensor, stream):
-        if not t.is_cuda:
-            raise ValueError("expected a GPU tensor")
-        if stream is not None and stream.device != t.device:
-            raise ValueError(f"stream is on {stream.device}, the tensors on {t.device}")
-        self.stream = torch.cuda.current_stream(t.device) if stream is None else stream
-        self._ctx = torch.cuda.stream(self.stream)
 
-    def __enter__(self):
-        self._ctx.__enter__()
-        return self.stream.cuda_stream
+def _elsewhere(t: torch.Tensor, stream) -> bool:
+    """Whether a call on t has to enter another device or stream first (_on)."""
+    if not t.is_cuda:
+        raise ValueError("expected a GPU tensor")
+    return stream is not None or t.get_device() != torch.cuda.current_device()
 
-    def __exit__(self, *exc):
-        return self._ctx.__exit__(*exc)
+
+def _on(t: torch.Tensor, stream):
+    """Makes t's device current and the given stream, or the device's current
+    one: outputs are then allocated for the stream that writes them."""
+    if stream is None:
+        stream = torch.cuda.current_stream(t.device)
+    elif stream.device != t.device:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {t.device}")
+    return torch.cuda.stream(stream)
 
 
 def _want_rows(t: torch.Tensor, name: str, shape, dtype, device):
     """As _want, for a matrix whose rows may be further apart than their length."""
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+    if t.shape != shape or t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, x on {device}")
-    if t.shape[1] > 1 and t.stride(1) != 1 or t.shape[0] > 1 and t.stride(0) < t.shape[1]:
+    _check_rows(t, name)
+
+
+def _check_rows(t: torch.Tensor, name: str):
+    if not t.is_contiguous() and (t.shape[1] > 1 and t.stride(1) != 1
+                                  or t.shape[0] > 1 and t.stride(0) < t.shape[1]):
         raise ValueError(f"the columns of {name} must be contiguous and its rows apart")
 
 
@@ -555,9 +562,10 @@ def _row_stride(t: torch.Tensor) -> int:
 
 
 def _float_type(dtype, name: str) -> int:
-    if dtype not in _FLOAT_TYPES:
+    t = _FLOAT_TYPES.get(dtype)
+    if t is None:
         raise ValueError(f"{name} must be bfloat16 or float32, got {dtype}")
-    return _FLOAT_TYPES[dtype]
+    return t
 
 
 def _want_fp8_rows(x: Fp8Rows):
@@ -582,60 +590,77 @@ def fp8_quantize_rows(x: torch.Tensor, swiglu: bool = False, stream=None,
                       out: Optional[Fp8Rows] = None) -> Fp8Rows:
     """x bfloat16 or float32 [M][K] -> E4M3 rows; swiglu: x [M][2K], of
     silu(x[:, :K]) * x[:, K:]. Rows of x may be strided."""
+    if _elsewhere(x, stream):
+        with _on(x, stream):
+            return fp8_quantize_rows(x, swiglu, None, out)
     if x.dim() != 2 or (swiglu and x.shape[1] % 2):
         raise ValueError("x must be [M][K], or [M][2K] with swiglu")
     xt = _float_type(x.dtype, "x")
-    M, K = x.shape[0], x.shape[1] // 2 if swiglu else x.shape[1]
-    _want_rows(x, "x", x.shape, x.dtype, x.device)
-    with _On(x, stream) as s:
-        if out is None:
-            out = Fp8Rows(torch.empty((M, K), dtype=torch.uint8, device=x.device),
-                          torch.empty((_blocks128(K), M), dtype=torch.float32, device=x.device))
+    _check_rows(x, "x")
+    M, K = x.shape
+    ldx = _row_stride(x)
+    if swiglu:
+        K //= 2
+    if out is None:
+        dev = x.device
+        out = Fp8Rows(torch.empty((M, K), dtype=torch.uint8, device=dev),
+                      torch.empty((_blocks128(K), M), dtype=torch.float32, device=dev))
+    else:
         _want(out.codes, "out.codes", (M, K), torch.uint8, x.device)
         _want(out.scales, "out.scales", (_blocks128(K), M), torch.float32, x.device)
-        _check(lib.fp8_quantize_rows(x.data_ptr(), xt, M, K, _row_stride(x), int(swiglu),
-                                     _ptr(out.codes), _ptr(out.scales), s), "fp8_quantize_rows")
+    _check(lib.fp8_quantize_rows(x.data_ptr(), xt, M, K, ldx, swiglu, out.codes.data_ptr(),
+                                 out.scales.data_ptr(), _raw_stream(x.get_device())),
+           "fp8_quantize_rows")
     return out
 
 
 def fp8_quantize_blocks(w: torch.Tensor, stream=None,
                         out: Optional[Fp8Blocks] = None) -> Fp8Blocks:
     """w bfloat16 or float32 [G][N][K] (or [N][K]: G = 1) -> E4M3 weights."""
+    if _elsewhere(w, stream):
+        with _on(w, stream):
+            return fp8_quantize_blocks(w, None, out)
     wt = _float_type(w.dtype, "w")
     if w.dim() == 2:
         w = w.unsqueeze(0)
     if w.dim() != 3:
         raise ValueError("w must be [G][N][K] or [N][K]")
     G, N, K = w.shape
-    with _On(w, stream) as s:
-        if out is None:
-            out = Fp8Blocks(torch.empty((G, N, K), dtype=torch.uint8, device=w.device),
-                            torch.empty((G, _blocks128(N), _blocks128(K)), dtype=torch.float32,
-                                        device=w.device))
-        _want(out.codes, "out.codes", (G, N, K), torch.uint8, w.device)
-        _want(out.scales, "out.scales", (G, _blocks128(N), _blocks128(K)), torch.float32,
-              w.device)
-        _check(lib.fp8_quantize_blocks(_ptr(w), wt, G, N, K, _ptr(out.codes), _ptr(out.scales),
-                                       s), "fp8_quantize_blocks")
+    dev = w.device
+    if out is None:
+        out = Fp8Blocks(torch.empty((G, N, K), dtype=torch.uint8, device=dev),
+                        torch.empty((G, _blocks128(N), _blocks128(K)), dtype=torch.float32,
+                                    device=dev))
+    else:
+        _want(out.codes, "out.codes", (G, N, K), torch.uint8, dev)
+        _want(out.scales, "out.scales", (G, _blocks128(N), _blocks128(K)), torch.float32, dev)
+    _check(lib.fp8_quantize_blocks(_ptr(w), wt, G, N, K, out.codes.data_ptr(),
+                                   out.scales.data_ptr(), _raw_stream(w.get_device())),
+           "fp8_quantize_blocks")
     return out
 
 
 def fp8_block_gemm(x: Fp8Rows, w: Fp8Blocks, out_dtype: torch.dtype = torch.bfloat16,
                    stream=None, out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """x [M][K], w G = 1 [N][K] -> out_dtype [M][N] = x w^T. Rows of out may be strided."""
+    if _elsewhere(x.codes, stream):
+        with _on(x.codes, stream):
+            return fp8_block_gemm(x, w, out_dtype, None, out)
     M, K = _want_fp8_rows(x)
     dev = x.codes.device
     G, N = _want_fp8_blocks(w, K, dev)
     if G != 1:
         raise ValueError("w must hold one matrix")
     yt = _float_type(out_dtype, "out_dtype")
-    with _On(x.codes, stream) as s:
-        if out is None:
-            out = torch.empty((M, N), dtype=out_dtype, device=dev)
+    if out is None:
+        out = torch.empty((M, N), dtype=out_dtype, device=dev)
+        ldy = N
+    else:
         _want_rows(out, "out", (M, N), out_dtype, dev)
-        _check(lib.fp8_block_gemm(_ptr(x.codes), _ptr(x.scales), M, K, _ptr(w.codes),
-                                  _ptr(w.scales), N, out.data_ptr(), yt, _row_stride(out), s),
-               "fp8_block_gemm")
+        ldy = _row_stride(out)
+    _check(lib.fp8_block_gemm(x.codes.data_ptr(), x.scales.data_ptr(), M, K, w.codes.data_ptr(),
+                              w.scales.data_ptr(), N, out.data_ptr(), yt, ldy,
+                              _raw_stream(x.codes.get_device())), "fp8_block_gemm")
     return out
 
 
@@ -645,45 +670,51 @@ def moe_grouped_gemm(x, routing: Routing, w, out_dtype: torch.dtype = torch.bflo
     or x Fp8Rows with w Fp8Blocks -> out_dtype [M k][N] in pair order. rows is M
     (token rows: pair p reads row p // k) or M k (pair p reads row p). Rows of
     out may be strided; those of pairs in no active slot are left as they were."""
-    M, k = routing.ids.shape
-    R = M * k
     fp8 = isinstance(x, Fp8Rows)
     if fp8 != isinstance(w, Fp8Blocks):
         raise ValueError("x and w must both be FP8 (Fp8Rows, Fp8Blocks) or both bfloat16")
+    xc = x.codes if fp8 else x
+    if _elsewhere(xc, stream):
+        with _on(xc, stream):
+            return moe_grouped_gemm(x, routing, w, out_dtype, None, out)
+    M, k = routing.ids.shape
+    R = M * k
+    dev = xc.device
     a = GroupedArgs()
     if fp8:
         rows, K = _want_fp8_rows(x)
-        xc, dev = x.codes, x.codes.device
         E, N = _want_fp8_blocks(w, K, dev)
-        a.x, a.x_scales = _ptr(x.codes), _ptr(x.scales)
-        a.w, a.w_scales = _ptr(w.codes), _ptr(w.scales)
-        a.type = NVFP4MOE_FP8
+        a.x_scales, a.w_scales = x.scales.data_ptr(), w.scales.data_ptr()
+        a.w, a.type = w.codes.data_ptr(), NVFP4MOE_FP8
     else:
         if x.dim() != 2 or w.dim() != 3 or x.shape[1] != w.shape[2]:
             raise ValueError("need x [rows][K] and w [E][N][K]")
-        xc, dev = x, x.device
         rows, K = x.shape
         E, N = w.shape[:2]
         _want(x, "x", (rows, K), torch.bfloat16, dev)
         _want(w, "w", (E, N, K), torch.bfloat16, dev)
-        a.x, a.w, a.type = _ptr(x), _ptr(w), NVFP4MOE_BF16
-    if rows not in (M, R):
+        a.w, a.type = w.data_ptr(), NVFP4MOE_BF16
+    if rows != M and rows != R:
         raise ValueError(f"x has {rows} rows: need {M} (token rows) or {R} (a row per pair)")
     for name, t, n in (("pairs", routing.pairs, R), ("active", routing.active, E),
                        ("active_offsets", routing.active_offsets, E + 1),
                        ("n_active", routing.n_active, 1)):
         _want(t, name, (n,), torch.int32, dev)
-    a.pairs, a.active = _ptr(routing.pairs), _ptr(routing.active)
-    a.active_offsets, a.n_active = _ptr(routing.active_offsets), _ptr(routing.n_active)
+    a.x = xc.data_ptr()
+    a.pairs, a.active = routing.pairs.data_ptr(), routing.active.data_ptr()
+    a.active_offsets, a.n_active = routing.active_offsets.data_ptr(), routing.n_active.data_ptr()
     a.R, a.x_rows, a.pairs_per_row = R, rows, 1 if rows == R else k
     a.E, a.N, a.K = E, N, K
     a.y_type = _float_type(out_dtype, "out_dtype")
-    with _On(xc, stream) as s:
-        if out is None:
-            out = torch.empty((R, N), dtype=out_dtype, device=dev)
+    if out is None:
+        out = torch.empty((R, N), dtype=out_dtype, device=dev)
+        a.ldy = N
+    else:
         _want_rows(out, "out", (R, N), out_dtype, dev)
-        a.y, a.ldy = out.data_ptr(), _row_stride(out)
-        _check(lib.moe_grouped_gemm(ctypes.byref(a), s), "moe_grouped_gemm")
+        a.ldy = _row_stride(out)
+    a.y = out.data_ptr()
+    _check(lib.moe_grouped_gemm(ctypes.byref(a), _raw_stream(xc.get_device())),
+           "moe_grouped_gemm")
     return out
 
 
@@ -692,6 +723,9 @@ def moe_combine(y: torch.Tensor, w: torch.Tensor, shared: Optional[torch.Tensor]
                 out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """y bfloat16 or float32 [M k][H], w float32 [M][k] (+ shared [M][H] of y's
     type, residual bfloat16 [M][H]) -> bfloat16 [M][H]."""
+    if _elsewhere(y, stream):
+        with _on(y, stream):
+            return moe_combine(y, w, shared, residual, None, out)
     if y.dim() != 2 or w.dim() != 2:
         raise ValueError("need y [M k][H] and w [M][k]")
     yt = _float_type(y.dtype, "y")
@@ -702,10 +736,12 @@ def moe_combine(y: torch.Tensor, w: torch.Tensor, shared: Optional[torch.Tensor]
     _want(w, "w", (M, k), torch.float32, dev)
     _want(shared, "shared", (M, H), y.dtype, dev)
     _want(residual, "residual", (M, H), torch.bfloat16, dev)
-    with _On(y, stream) as s:
-        if out is None:
-            out = torch.empty((M, H), dtype=torch.bfloat16, device=dev)
+    if out is None:
+        out = torch.empty((M, H), dtype=torch.bfloat16, device=dev)
+    else:
         _want(out, "out", (M, H), torch.bfloat16, dev)
-        _check(lib.moe_combine(_ptr(y), yt, _ptr(w), _ptr(shared), _ptr(residual), M, k, H,
-                               _ptr(out), s), "moe_combine")
+    _check(lib.moe_combine(y.data_ptr(), yt, w.data_ptr(),
+                           None if shared is None else shared.data_ptr(),
+                           None if residual is None else residual.data_ptr(), M, k, H,
+                           out.data_ptr(), _raw_stream(y.get_device())), "moe_combine")
     return out
