@@ -783,11 +783,11 @@ int32_t launch_direct(const BlockGemmParams& p, const char* what, hipStream_t s)
   return launched(what);
 }
 
-template <Mma MODE, bool GROUPED, int BN, int BM, int WVN, int WVM, int S, typename Y>
+template <Mma MODE, bool GROUPED, int BN, int BM, int WVN, int WVM, typename Y>
 int32_t launch_tiled(const BlockGemmParams& p, const char* what, hipStream_t s) {
   const int64_t grid = block_gemm_grid(p, GROUPED, BN, BM);
   if (grid < 0) return grid_too_large(what);
-  hipLaunchKernelGGL((tiled_gemm_kernel<MODE, GROUPED, BN, BM, WVN, WVM, S, Y>),
+  hipLaunchKernelGGL((tiled_gemm_kernel<MODE, GROUPED, BN, BM, WVN, WVM, Y>),
                      dim3((unsigned)grid), dim3(WVN * WVM * 64), 0, s, p, (p.N + BN - 1) / BN);
   return launched(what);
 }
@@ -818,16 +818,17 @@ int32_t launch_block_gemm(const BlockGemmParams& p, const char* what, hipStream_
   const int64_t small = p.slots * tiles_of(per_slot, 64) * tiles_of(p.N, 64);
   if constexpr (GROUPED) {
     if (per_slot <= 8 && direct <= 1024) return launch_direct<kExact, GROUPED, Y>(p, what, s);
-    if (per_slot <= 16) return launch_tiled<kFast, GROUPED, 128, 32, 4, 1, 3, Y>(p, what, s);
-    if (small <= 640) return launch_tiled<kFast, GROUPED, 64, 64, 2, 2, 3, Y>(p, what, s);
-    if (per_slot < 48) return launch_tiled<kFast, GROUPED, 128, 64, 2, 2, 3, Y>(p, what, s);
+    if (per_slot <= 16) return launch_tiled<kFast, GROUPED, 128, 32, 4, 1, Y>(p, what, s);
+    if (small <= 640) return launch_tiled<kFast, GROUPED, 64, 64, 2, 2, Y>(p, what, s);
+    if (per_slot < 48) return launch_tiled<kFast, GROUPED, 128, 64, 2, 2, Y>(p, what, s);
   } else {
     if (direct <= 640) return launch_direct<kExact, GROUPED, Y>(p, what, s);
-    if (p.R <= 32) return launch_tiled<kFast, GROUPED, 128, 32, 4, 1, 3, Y>(p, what, s);
-    if (small <= 640) return launch_tiled<kFast, GROUPED, 64, 64, 2, 2, 3, Y>(p, what, s);
-    if (small <= 2560) return launch_tiled<kFast, GROUPED, 128, 64, 2, 2, 3, Y>(p, what, s);
+    if (p.R <= 32) return launch_tiled<kFast, GROUPED, 128, 32, 4, 1, Y>(p, what, s);
+    if (small <= 640) return launch_tiled<kFast, GROUPED, 64, 64, 2, 2, Y>(p, what, s);
+    if (small <= 2560) return launch_tiled<kFast, GROUPED, 128, 64, 2, 2, Y>(p, what, s);
   }
-  return launch_tiled<kFast, GROUPED, 256, 128, 4, 2, 3, Y>(p, what, s);
+  return launch_tiled<kFast, GROUPED, GROUPED ? 256 : 128, GROUPED ? 128 : 256, GROUPED ? 4 : 2,
+                      GROUPED ? 2 : 4, Y>(p, what, s);
 }
 
 }  // namespace

@@ -33,6 +33,8 @@
 // p / div and writes y row p. Tiles hold rows of one slot only.
 #pragma once
 
+#include <utility>
+
 #include "block8.hpp"
 #include "fp8.hpp"
 
@@ -43,6 +45,18 @@ typedef float bg_f32x4 __attribute__((ext_vector_type(4)));
 typedef int bg_i32x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kStepBytes = 128;
+
+// f(0), ..., f(N - 1) with the index a constant expression: arrays indexed by
+// it are registers from the start (indexed by the counter of a loop that is
+// unrolled later, the compiler moved one of them to LDS).
+template <typename F, int... I>
+__device__ __forceinline__ void static_for(F& f, std::integer_sequence<int, I...>) {
+  (f(std::integral_constant<int, I>{}), ...);
+}
+template <int N, typename F>
+__device__ __forceinline__ void static_for(F f) {
+  static_for(f, std::make_integer_sequence<int, N>{});
+}
 
 struct BlockGemmParams {
   const uint8_t* x;   // [Mx][row_bytes]
@@ -427,13 +441,31 @@ __global__ void __launch_bounds__(kDirectWaves * 64) direct_gemm_kernel(BlockGem
 //
 // One block per (row tile of BM rows, BN weight rows), wave tiles of
 // BN / WVN x BM / WVM. A k step of the BN + BM rows (128 bytes each, and the x
-// scales) is copied to LDS by direct loads; with S stages, S - 1 steps are in
-// flight or ready while one is multiplied.
-// Piece c of row r lies at piece c ^ (r % 8) of the row's 128 bytes, so lanes
-// that read the same piece of neighbouring rows hit different banks (no bank
-// conflict counted in the loop); the copy's lanes are contiguous in LDS, so
-// the exchange is made on the global side (eight lanes still read one row's
-// whole 128 bytes).
+// scales) is copied to one of three LDS stages by direct loads, 16 bytes a
+// lane, two steps ahead of its products. Piece c of row r lies at piece
+// c ^ (r % 8) of the row's 128 bytes, so lanes that read the same piece of
+// neighbouring rows hit different banks (no bank conflict counted in the
+// loop); a copy's lanes are contiguous in LDS, so the exchange is made on the
+// global side (eight lanes still read one row's whole 128 bytes).
+//
+// Order within step k, for a wave with NT rows of MT product tiles: its first
+// operands (two weight and MT x operands, the scales) are already in
+// registers; weight operand i + 2 is read while row i is multiplied, and the
+// copies of step k + 2 go out between the products, into the stage of step
+// k - 1; before the last row, one barrier: step k + 1 is complete and nobody
+// reads this stage any more; during the last row the first operands of step
+// k + 1 replace those just used. So the matrix cores have work across the
+// barrier (with the barrier between the steps and the operands read after it:
+// grouped gate_up 2048 -> 1024 at M = 4 15.0 us, this way 13.2), and a copy has
+// more than a step to arrive (with two stages and one step: M = 16 53 us,
+// this way 44; more than three stages only cost blocks per CU).
+//
+// What bounds large products (M = 8192, 2048 -> 5120: 95 us, 1.8 PFLOP/s): the
+// products and scalings alone run at about 2.8 PFLOP/s (K = 8192; matrix
+// instructions and scalings without operands at 4.0, at the clock of about
+// 2 GHz that the chip holds under them); the copies into LDS beside the
+// operand reads cost the rest (a 1 KB direct load about 24 clocks of the LDS, a
+// 1 KB read 4; through registers and LDS stores it took the same time).
 typedef __attribute__((address_space(3))) void lds_void;
 typedef const __attribute__((address_space(1))) void global_void;
 
@@ -445,14 +477,19 @@ __device__ __forceinline__ void copy4_to_lds(const float* src, uint8_t* dst) {
   __builtin_amdgcn_global_load_lds((global_void*)src, (lds_void*)dst, 4, 0, 0);
 }
 
-// Waits until at most N of the wave's vector memory requests are outstanding.
+// All of the wave's requests but the N newest loads are done, then those of
+// every wave of the block.
 template <int N>
-__device__ __forceinline__ void wait_vmem() {
+__device__ __forceinline__ void arrive() {
   static_assert(N >= 0 && N < 64, "");
-  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
 }
 
-template <Mma MODE, bool GROUPED, int BN, int BM, int WVN, int WVM, int S, typename Y>
+template <Mma MODE, bool GROUPED, int BN, int BM, int WVN, int WVM>
 struct Tiled {
   static constexpr bool FP8 = MODE != Mma::kBf16;
   static constexpr int kWaves = WVN * WVM, kThreads = kWaves * 64;
@@ -465,7 +502,8 @@ struct Tiled {
   static constexpr int kStageBytes = kScales + kWaves * LS * 256;
   static_assert(LA * 8 * kWaves == BN && LB * 8 * kWaves == BM, "rows split evenly over the waves");
   static_assert(kBlock8 % WN == 0, "a wave's weight rows share a scale block");
-  static_assert(S * kStageBytes <= 160 * 1024, "the stages fit the LDS");
+  static_assert(NT % 2 == 0, "the first weight operand of a step is always a[0]");
+  static_assert(3 * kStageBytes <= 160 * 1024, "the stages fit the LDS");
 
   // What a lane copies: byte offsets of its rows (weights: from the tile's
   // first row; x: from the tile's first row, or of any row when gathered),
@@ -476,112 +514,148 @@ struct Tiled {
     uint32_t s[LS ? LS : 1];
   };
 
-  // Copies a step into a stage. w, x, xs: the bases plus the step's offset.
-  // Pieces past K read the step's first piece (zeroed after the read from LDS).
-  static __device__ __forceinline__ void copy(const Rows& r, const uint8_t* w, const uint8_t* x,
-                                              const float* xs, int base, int piece, int row_bytes,
-                                              int wave, uint8_t* stage) {
-    const uint32_t o = base + 16 * piece < row_bytes ? 16 * piece : 0;
-#pragma unroll
-    for (int j = 0; j < LA; ++j)
-      copy16_to_lds(w + (uint32_t)(r.a[j] + o), stage + (j * kWaves + wave) * 1024);
-#pragma unroll
-    for (int j = 0; j < LB; ++j)
-      copy16_to_lds(x + (GROUPED ? r.b[j] + o : (uint32_t)((uint32_t)r.b[j] + o)),
-                      stage + BN * kStepBytes + (j * kWaves + wave) * 1024);
-#pragma unroll
-    for (int j = 0; j < LS; ++j)
-      copy4_to_lds(xs + r.s[j], stage + kScales + (wave * LS + j) * 256);
+  // The step that is being copied: bases plus the step's offset, and the
+  // lane's piece of its rows (past K: the step's first piece, zeroed after the
+  // read from LDS). After the last step the last one is copied again.
+  struct Cursor {
+    const uint8_t *w, *x;
+    const float* xs;
+    uint32_t o;
+    int step;
+    __device__ __forceinline__ void set_piece(const BlockGemmParams& p, int piece) {
+      o = step * kStepBytes + 16 * piece < p.row_bytes ? 16 * piece : 0;
+    }
+    __device__ __forceinline__ void advance(const BlockGemmParams& p, int piece) {
+      const int more = step + 1 < p.KB ? 1 : 0;  // no branch: the compiler would move the
+      step += more;                              // scaling of the products behind it
+      w += more * kStepBytes;
+      x += more * kStepBytes;
+      if constexpr (FP8) xs += more * p.Mx;
+      set_piece(p, piece);
+    }
+  };
+
+  // Copy i of the cursor's step into a stage.
+  template <int i>
+  static __device__ __forceinline__ void copy(const Rows& r, const Cursor& c, int wave,
+                                              uint8_t* stage) {
+    if constexpr (i < LA) {
+      copy16_to_lds(c.w + (uint32_t)(r.a[i] + c.o), stage + (i * kWaves + wave) * 1024);
+    } else if constexpr (i < LA + LB) {
+      constexpr int j = i - LA;
+      copy16_to_lds(c.x + (GROUPED ? r.b[j] + c.o : (uint32_t)((uint32_t)r.b[j] + c.o)),
+                    stage + BN * kStepBytes + (j * kWaves + wave) * 1024);
+    } else {
+      constexpr int j = i - LA - LB;
+      copy4_to_lds(c.xs + r.s[j], stage + kScales + (wave * LS + j) * 256);
+    }
   }
 
-  // TAIL: the last step, which may end past K (k0, k1: masks of the lane's pieces).
-  template <bool TAIL>
-  static __device__ __forceinline__ Frag read(const uint8_t* rows, int row, int lo, uint32_t k0,
-                                              uint32_t k1) {
-    const uint8_t* r = rows + row * kStepBytes;
+  // A wave's place in a stage.
+  struct Place {
+    int w, x, s;  // byte offsets of the lane's first weight row, x row and scale
+    int lo;       // the lane's first piece of a row (the second: lo ^ 64)
+    __device__ __forceinline__ Place(int wave, int wn, int wm, int lane) {
+      const int c = lane & 15, g = lane >> 4;
+      w = (wn + c) * kStepBytes;
+      x = (BN + wm + c) * kStepBytes;
+      s = kScales + wave * LS * 256 + 4 * c;
+      lo = 16 * (g ^ (c & 7));
+    }
+  };
+
+  static __device__ __forceinline__ Frag read(const uint8_t* row, int lo) {
     Frag f;
-    f.lo = *reinterpret_cast<const uint4*>(r + lo);
-    f.hi = *reinterpret_cast<const uint4*>(r + (lo ^ 64));
-    if constexpr (TAIL) mask_frag(f, k0, k1);
+    f.lo = *reinterpret_cast<const uint4*>(row + lo);
+    f.hi = *reinterpret_cast<const uint4*>(row + (lo ^ 64));
     return f;
   }
 
-  // The products of one step; ahead() requests a later step once this step's
-  // first operands are requested. FP8: a tile's block sum is scaled into the
-  // result two instructions later, while the matrix cores work on (the
-  // scheduling barriers keep that order: left alone, the compiler moves the
-  // scaling next to its product and waits there).
-  template <bool TAIL, typename Ahead>
-  static __device__ __forceinline__ void products(const uint8_t* stage, int base, int row_bytes,
-                                                  int wave, int wn, int wm, int lane, float ws,
-                                                  bg_f32x4 (&acc)[NT][MT], Ahead ahead) {
-    constexpr int kLag = NT * MT >= 2 ? 2 : 1;
-    const int c = lane & 15, g = lane >> 4;
-    const int lo = 16 * (g ^ (c & 7));
-    const uint32_t k0 = base + 16 * g < row_bytes ? ~0u : 0u;
-    const uint32_t k1 = base + 64 + 16 * g < row_bytes ? ~0u : 0u;
-    const uint8_t* wrows = stage + (wn + c) * kStepBytes;
-    const uint8_t* xrows = stage + (BN + wm + c) * kStepBytes;
-    const float* xs = reinterpret_cast<const float*>(stage + kScales + wave * LS * 256) + c;
-    Operand<MODE> b[MT], a[2];
+  // The first operands of a step.
+  struct First {
+    Frag a[2], b[MT];
+    float xs[MT];
+    template <int j>
+    __device__ __forceinline__ void read_b(const uint8_t* stage, const Place& at) {
+      b[j] = read(stage + at.x + 16 * j * kStepBytes, at.lo);
+    }
+    __device__ __forceinline__ void read_a(const uint8_t* stage, const Place& at) {
+      a[0] = read(stage + at.w, at.lo);
+      a[1] = read(stage + at.w + 16 * kStepBytes, at.lo);
+    }
+    __device__ __forceinline__ void read_xs(const uint8_t* stage, const Place& at) {
+#pragma unroll
+      for (int j = 0; j < MT; ++j)
+        xs[j] = FP8 ? *reinterpret_cast<const float*>(stage + at.s + 64 * j) : 1.0f;
+    }
+  };
+
+  // One step, held by cur. LAST: the last one, which may end past K (k0, k1:
+  // masks of the lane's pieces); otherwise late(i) makes copy i of step k + 1
+  // into the other stage, turn() moves on to step k + 2, early(i) makes its
+  // copies into cur.
+  // FP8: a tile's block sum is scaled into the result two instructions later,
+  // while the matrix cores work on (the scheduling barriers keep that order:
+  // left alone, the compiler moves the scaling next to its product and waits
+  // there).
+  template <bool LAST, typename Ahead>
+  static __device__ __forceinline__ void step(const uint8_t* cur, const uint8_t* other,
+                                              const Place& at, First& f, float ws, uint32_t k0,
+                                              uint32_t k1, bg_f32x4 (&acc)[NT][MT], Ahead ahead) {
+    Frag a[3];  // rows i, i + 1 and i + 2 at i mod 3
+    a[0] = f.a[0];
+    a[1] = f.a[1];
+    Operand<MODE> b[MT];
     float s[MT];
-    // x operands that are requested before the first product; the others
-    // follow one product behind another, so that the first ones need not wait
-    // for all of them (LDS answers in order, and every wave asks at once)
-    constexpr int kFirst = MODE == Mma::kFp8 && MT > 2 ? 2 : MT;
-    a[0].set(read<TAIL>(wrows, 0, lo, k0, k1));
-    __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-    for (int j = 0; j < kFirst; ++j) {
-      b[j].set(read<TAIL>(xrows, 16 * j, lo, k0, k1));
-      __builtin_amdgcn_sched_barrier(0);
+    if constexpr (LAST) {
+      mask_frag(a[0], k0, k1);
+      mask_frag(a[1], k0, k1);
     }
-    ahead();
-    __builtin_amdgcn_sched_barrier(0);
-    if constexpr (kFirst == MT) {
 #pragma unroll
-      for (int j = 0; j < MT; ++j) s[j] = FP8 ? xs[16 * j] : 1.0f;
+    for (int j = 0; j < MT; ++j) {
+      if constexpr (LAST) mask_frag(f.b[j], k0, k1);
+      b[j].set(f.b[j]);
+      s[j] = f.xs[j] * ws;
     }
+    auto weights_ahead = [&](auto row) {
+      a[row % 3] = read(cur + at.w + 16 * row * kStepBytes, at.lo);
+      if constexpr (LAST) mask_frag(a[row % 3], k0, k1);
+    };
     if constexpr (MODE == Mma::kFp8) {
+      constexpr int kLag = 3;
       bg_f32x4 t[kLag + 1];
-#pragma unroll
-      for (int i = 0; i < NT; ++i) {
-#pragma unroll
-        for (int j = 0; j < MT; ++j) {
-          const int q = i * MT + j, d = q - kLag;
-          t[q % (kLag + 1)] = block_mma<MODE>(a[i & 1], b[j]);
-          __builtin_amdgcn_sched_barrier(0);
-          if (i == 0 && j + kFirst < MT) {
-            b[j + kFirst].set(read<TAIL>(xrows, 16 * (j + kFirst), lo, k0, k1));
-            __builtin_amdgcn_sched_barrier(0);
-          }
-          if (kFirst < MT && q == 0) {
-#pragma unroll
-            for (int v = 0; v < MT; ++v) s[v] = xs[16 * v];
-            __builtin_amdgcn_sched_barrier(0);
-          }
-          if (i == 0 && kFirst == MT) s[j] *= ws;
-          if (kFirst < MT && q == 1) {
-#pragma unroll
-            for (int v = 0; v < MT; ++v) s[v] *= ws;
-          }
-          if (d >= 0) scale_into(t[d % (kLag + 1)], s[d % MT], acc[d / MT][d % MT]);
-          if (j == 0 && i + 1 < NT)
-            a[(i + 1) & 1].set(read<TAIL>(wrows, 16 * (i + 1), lo, k0, k1));
-          __builtin_amdgcn_sched_barrier(0);
+      static_for<NT * MT>([&](auto qc) {
+        constexpr int q = qc, i = q / MT, j = q % MT, d = q - kLag;
+        if constexpr (!LAST && i == NT - 1 && j == 0) arrive<kCopies>();
+        Operand<MODE> ao;
+        ao.set(a[i % 3]);
+        t[q % (kLag + 1)] = block_mma<MODE>(ao, b[j]);
+        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (j == 0 && i + 2 < NT) weights_ahead(std::integral_constant<int, i + 2>{});
+        if constexpr (!LAST && i == NT - 1) {
+          if constexpr (j == 0) f.read_a(other, at);
+          f.template read_b<j>(other, at);
+          if constexpr (j == MT - 1) f.read_xs(other, at);
         }
-      }
+        if constexpr (d >= 0) scale_into(t[d % (kLag + 1)], s[d % MT], acc[d / MT][d % MT]);
+        if constexpr (!LAST && i < NT - 1)
+          static_for<kCopies>([&](auto v) {
+            if constexpr (v * (NT - 1) * MT / kCopies == q) ahead(v);
+          });
+        __builtin_amdgcn_sched_barrier(0);
+      });
 #pragma unroll
       for (int d = NT * MT - kLag; d < NT * MT; ++d)
         scale_into(t[d % (kLag + 1)], s[d % MT], acc[d / MT][d % MT]);
     } else {
       // several instructions per tile and step: those of a row of tiles in
       // turn, so that none waits for the one before it
-      constexpr int kParts = (int)(sizeof(a[0].v) / sizeof(a[0].v[0]));
-#pragma unroll
-      for (int j = 0; j < MT; ++j) s[j] *= ws;
-#pragma unroll
-      for (int i = 0; i < NT; ++i) {
+      constexpr int kParts = (int)(sizeof(Operand<MODE>::v) / sizeof(bg_bf16x8));
+      static_for<NT>([&](auto ic) {
+        constexpr int i = ic;
+        if constexpr (!LAST && i == NT - 1) arrive<kCopies>();
+        Operand<MODE> ao;
+        ao.set(a[i % 3]);
         bg_f32x4 t[MT];
 #pragma unroll
         for (int j = 0; j < MT; ++j) t[j] = FP8 ? bg_f32x4{0.0f, 0.0f, 0.0f, 0.0f} : acc[i][j];
@@ -589,8 +663,17 @@ struct Tiled {
         for (int e = 0; e < kParts; ++e)
 #pragma unroll
           for (int j = 0; j < MT; ++j)
-            t[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[i & 1].v[e], b[j].v[e], t[j], 0, 0, 0);
-        if (i + 1 < NT) a[(i + 1) & 1].set(read<TAIL>(wrows, 16 * (i + 1), lo, k0, k1));
+            t[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ao.v[e], b[j].v[e], t[j], 0, 0, 0);
+        if constexpr (i + 2 < NT) weights_ahead(std::integral_constant<int, i + 2>{});
+        if constexpr (!LAST && i == NT - 1) {
+          f.read_a(other, at);
+          static_for<MT>([&](auto j) { f.template read_b<j>(other, at); });
+          f.read_xs(other, at);
+        }
+        if constexpr (!LAST && i < NT - 1)
+          static_for<kCopies>([&](auto v) {
+            if constexpr (v * (NT - 1) / kCopies == i) ahead(v);
+          });
 #pragma unroll
         for (int j = 0; j < MT; ++j) {
           if constexpr (FP8)
@@ -598,7 +681,7 @@ struct Tiled {
           else
             acc[i][j] = t[j];
         }
-      }
+      });
     }
   }
 };
@@ -616,11 +699,11 @@ __device__ __forceinline__ void pack4(const bg_f32x4& v, float* dst) {
   *reinterpret_cast<bg_f32x4*>(dst) = v;
 }
 
-template <Mma MODE, bool GROUPED, int BN, int BM, int WVN, int WVM, int S, typename Y>
+template <Mma MODE, bool GROUPED, int BN, int BM, int WVN, int WVM, typename Y>
 __global__ void __launch_bounds__(WVN* WVM * 64, 2)
     tiled_gemm_kernel(BlockGemmParams p, int n_tiles) {
-  using T = Tiled<MODE, GROUPED, BN, BM, WVN, WVM, S, Y>;
-  __shared__ __align__(1024) uint8_t stages[S * T::kStageBytes];
+  using T = Tiled<MODE, GROUPED, BN, BM, WVN, WVM>;
+  __shared__ __align__(1024) uint8_t stages[3 * T::kStageBytes];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const Work work = block_work<BN, BM, GROUPED>(p, n_tiles, lane);
@@ -630,9 +713,19 @@ __global__ void __launch_bounds__(WVN* WVM * 64, 2)
 
   const int piece = (lane & 7) ^ (lane >> 3);
   const int wn = (wave % WVN) * T::WN, wm = (wave / WVN) * T::WM;
-  const uint8_t* wk = p.w + t.e * p.w_mat_bytes + (int64_t)n0 * p.row_bytes;
-  const uint8_t* xk = GROUPED ? p.x : p.x + (int64_t)t.row0 * p.row_bytes;
-  const float* xsk = p.xs;
+  // the weight scales of 64 steps, one a lane
+  const float* wsr = nullptr;
+  float ws_lanes = 1.0f;
+  if constexpr (T::FP8) {
+    wsr = p.ws + ((int64_t)t.e * p.NB + min((n0 + wn) / kBlock8, p.NB - 1)) * p.KB;
+    ws_lanes = wsr[min(lane, p.KB - 1)];
+  }
+  typename T::Cursor c;
+  c.w = p.w + t.e * p.w_mat_bytes + (int64_t)n0 * p.row_bytes;
+  c.x = GROUPED ? p.x : p.x + (int64_t)t.row0 * p.row_bytes;
+  c.xs = p.xs;
+  c.step = 0;
+  c.set_piece(p, piece);
   typename T::Rows rows;
 #pragma unroll
   for (int j = 0; j < T::LA; ++j) {
@@ -650,13 +743,6 @@ __global__ void __launch_bounds__(WVN* WVM * 64, 2)
 #pragma unroll
   for (int j = 0; j < T::LS; ++j)
     rows.s[j] = (uint32_t)x_row<GROUPED>(p, t, wm + 64 * j + (lane & (T::WM < 64 ? T::WM - 1 : 63)));
-  // the weight scales of 64 steps, one a lane
-  const float* wsr = nullptr;
-  float ws_lanes = 1.0f;
-  if constexpr (T::FP8) {
-    wsr = p.ws + ((int64_t)t.e * p.NB + min((n0 + wn) / kBlock8, p.NB - 1)) * p.KB;
-    ws_lanes = wsr[min(lane, p.KB - 1)];
-  }
 
   bg_f32x4 acc[T::NT][T::MT];
 #pragma unroll
@@ -664,73 +750,62 @@ __global__ void __launch_bounds__(WVN* WVM * 64, 2)
 #pragma unroll
     for (int j = 0; j < T::MT; ++j) acc[i][j] = {0.0f, 0.0f, 0.0f, 0.0f};
 
-  int issued = 0;  // steps requested so far
-  auto request = [&](uint8_t* __restrict__ stage) {
-    T::copy(rows, wk, xk, xsk, issued * kStepBytes, piece, p.row_bytes, wave, stage);
-    wk += kStepBytes;
-    xk += kStepBytes;
-    if constexpr (T::FP8) xsk += p.Mx;
-    ++issued;
-  };
-#pragma unroll
-  for (int q = 0; q < S - 1; ++q)
-    if (q < p.KB) request(stages + q * T::kStageBytes);
-  // (the empty asm is a use: the wait for this load stays here and in the
-  // reload's branch, instead of one for every request in every step)
+  // steps 0 and 1, and the first operands of step 0
+  static_for<2>([&](auto q) {
+    static_for<T::kCopies>(
+        [&](auto v) { T::template copy<v>(rows, c, wave, stages + q * T::kStageBytes); });
+    c.advance(p, piece);
+  });
+  // (a use: the wait for this load stays here, instead of one for everything
+  // outstanding in every step)
   asm volatile("" : "+v"(ws_lanes));
+  arrive<T::kCopies>();
+  const typename T::Place at(wave, wn, wm, lane);
+  typename T::First f;
+  f.read_a(stages, at);
+  static_for<T::MT>([&](auto j) { f.template read_b<j>(stages, at); });
+  f.read_xs(stages, at);
 
-  // Step kb, held by cur. Of the wave's requests only those of the steps after
-  // kb may be outstanding, then the barrier makes every wave's part of cur
-  // visible; it also says that every wave is done with the stage of step
-  // kb - 1, which is the one that is filled next.
-  auto arrive = [&](int kb) {
-    if (kb + S - 2 < p.KB)
-      wait_vmem<(S - 2) * T::kCopies>();
-    else
-      wait_vmem<0>();
-    __builtin_amdgcn_sched_barrier(0);
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
-    __builtin_amdgcn_sched_barrier(0);
-  };
   auto ws_of = [&](int kb) {
     if (T::FP8 && kb > 0 && (kb & 63) == 0) {
       ws_lanes = wsr[min(kb + lane, p.KB - 1)];
-      asm volatile("" : "+v"(ws_lanes));
+      asm volatile("" : "+v"(ws_lanes));  // as above
     }
     return T::FP8 ? __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(ws_lanes), kb & 63))
                   : 1.0f;
   };
-  auto step = [&](int kb, const uint8_t* __restrict__ cur, uint8_t* __restrict__ next) {
-    T::template products<false>(cur, kb * kStepBytes, p.row_bytes, wave, wn, wm, lane, ws_of(kb),
-                                acc, [&] {
-                                  if (issued < p.KB) request(next);
-                                });
+  auto step = [&](int kb, const uint8_t* __restrict__ cur, const uint8_t* __restrict__ next,
+                  uint8_t* __restrict__ fill) {
+    T::template step<false>(cur, next, at, f, ws_of(kb), ~0u, ~0u, acc,
+                            [&](auto v) { T::template copy<v>(rows, c, wave, fill); });
+    c.advance(p, piece);
   };
-  uint32_t at = 0, fill = (S - 1) * T::kStageBytes;
-  auto advance = [](uint32_t v) {
-    v += T::kStageBytes;
-    return v == S * T::kStageBytes ? 0u : v;
+  auto after = [](uint32_t stage) {
+    stage += T::kStageBytes;
+    return stage == 3 * T::kStageBytes ? 0u : stage;
   };
+  uint32_t cur = 0, fill = 2 * T::kStageBytes;
 #pragma unroll 1
   for (int kb = 0; kb + 1 < p.KB; ++kb) {
-    arrive(kb);
-    step(kb, stages + at, stages + fill);
-    at = advance(at);
-    fill = advance(fill);
+    step(kb, stages + cur, stages + after(cur), stages + fill);
+    cur = after(cur);
+    fill = after(fill);
   }
-  arrive(p.KB - 1);
-  T::template products<true>(stages + at, (p.KB - 1) * kStepBytes, p.row_bytes, wave, wn, wm, lane,
-                             ws_of(p.KB - 1), acc, [] {});
+  {
+    const int g = lane >> 4, base = (p.KB - 1) * kStepBytes;
+    const uint32_t k0 = base + 16 * g < p.row_bytes ? ~0u : 0u;
+    const uint32_t k1 = base + 64 + 16 * g < p.row_bytes ? ~0u : 0u;
+    T::template step<true>(stages + cur, stages, at, f, ws_of(p.KB - 1), k0, k1, acc, [](auto) {});
+  }
+  arrive<0>();  // the last reads, and copies that nothing needed
 
   // The results, 16 token rows at a time through the wave's own LDS: a lane
   // holds four n of one row, and the 16 rows of one store would take 32 bytes
   // each; read back, eight or more lanes write one row's consecutive 16-byte
   // pieces.
-  __syncthreads();  // the last step's reads
   constexpr int kRow = T::WN * (int)sizeof(Y) + 16, kPieces = T::WN * (int)sizeof(Y) / 16;
   constexpr int kPer = 16 / (int)sizeof(Y);  // elements of a piece
-  static_assert(T::kWaves * 16 * kRow <= S * T::kStageBytes, "the exchange fits the stages");
+  static_assert(T::kWaves * 16 * kRow <= 3 * T::kStageBytes, "the exchange fits the stages");
   uint8_t* ex = stages + wave * 16 * kRow;
   const bool aligned16 =
       (p.ldy % kPer | (int64_t)((uintptr_t)p.y % 16)) == 0;  // rows of y start on 16 bytes
