@@ -760,13 +760,12 @@ void launch_quantize_rows(const void* x, int64_t M, int64_t K, int64_t ldx, bool
                        (int)K, ldx, (int)KB, codes, scales);
 }
 
-// Blocks of BM x BN tiles, a multiple of eight (one part per XCD); grouped: of
-// the most row tiles that R rows in p.slots groups can take. < 0: too many.
-int64_t block_gemm_grid(const BlockGemmParams& p, bool grouped, int BN, int BM) {
+// The most tiles of BM x BN that a call can have; grouped: that R rows in
+// p.slots groups can take.
+int64_t block_gemm_tiles(const BlockGemmParams& p, bool grouped, int BN, int BM) {
   const int64_t n_tiles = (p.N + BN - 1) / BN;
   const int64_t rows = (int64_t)p.R + (grouped ? (int64_t)p.slots : 1) * (BM - 1);
-  const int64_t blocks = (n_tiles * (rows / BM) + 7) / 8 * 8;
-  return blocks > kMaxGrid ? -1 : blocks;
+  return n_tiles * (rows / BM);
 }
 
 int32_t grid_too_large(const char* what) {
@@ -776,19 +775,29 @@ int32_t grid_too_large(const char* what) {
 template <Mma MODE, bool GROUPED, typename Y>
 int32_t launch_direct(const BlockGemmParams& p, const char* what, hipStream_t s) {
   constexpr int NT = 1, MT = 1, U = 4;
-  const int64_t grid = block_gemm_grid(p, GROUPED, 16 * NT, 16 * MT);
-  if (grid < 0) return grid_too_large(what);
-  hipLaunchKernelGGL((direct_gemm_kernel<MODE, GROUPED, NT, MT, U, Y>), dim3((unsigned)grid),
-                     dim3(kDirectWaves * 64), 0, s, p, (p.N + 16 * NT - 1) / (16 * NT));
+  const int64_t tiles = block_gemm_tiles(p, GROUPED, 16 * NT, 16 * MT);
+  if (tiles > kMaxGrid - 7) return grid_too_large(what);
+  hipLaunchKernelGGL((direct_gemm_kernel<MODE, GROUPED, NT, MT, U, Y>),
+                     dim3((unsigned)((tiles + 7) / 8 * 8)), dim3(kDirectWaves * 64), 0, s, p,
+                     (p.N + 16 * NT - 1) / (16 * NT), (uint32_t)tiles);
   return launched(what);
 }
 
 template <Mma MODE, bool GROUPED, int BN, int BM, int WVN, int WVM, typename Y>
 int32_t launch_tiled(const BlockGemmParams& p, const char* what, hipStream_t s) {
-  const int64_t grid = block_gemm_grid(p, GROUPED, BN, BM);
-  if (grid < 0) return grid_too_large(what);
-  hipLaunchKernelGGL((tiled_gemm_kernel<MODE, GROUPED, BN, BM, WVN, WVM, Y>),
-                     dim3((unsigned)grid), dim3(WVN * WVM * 64), 0, s, p, (p.N + BN - 1) / BN);
+  const int64_t tiles = block_gemm_tiles(p, GROUPED, BN, BM);
+  if (tiles > kMaxGrid) return grid_too_large(what);
+  // a CU's worth of blocks for each of the 256 CUs, which share the tiles out
+  const int64_t fill = 256 * TiledLds<MODE, GROUPED, BN, BM, WVN, WVM>::kPerCu;
+  const dim3 block(WVN * WVM * 64);
+  const int n_tiles = (p.N + BN - 1) / BN;
+  if (tiles <= fill)
+    hipLaunchKernelGGL((tiled_gemm_kernel<MODE, GROUPED, BN, BM, WVN, WVM, false, Y>),
+                       dim3((unsigned)((tiles + 7) / 8 * 8)), block, 0, s, p, n_tiles,
+                       (uint32_t)tiles);
+  else
+    hipLaunchKernelGGL((tiled_gemm_kernel<MODE, GROUPED, BN, BM, WVN, WVM, true, Y>),
+                       dim3((unsigned)fill), block, 0, s, p, n_tiles, (uint32_t)tiles);
   return launched(what);
 }
 
@@ -827,8 +836,7 @@ int32_t launch_block_gemm(const BlockGemmParams& p, const char* what, hipStream_
     if (small <= 640) return launch_tiled<kFast, GROUPED, 64, 64, 2, 2, Y>(p, what, s);
     if (small <= 2560) return launch_tiled<kFast, GROUPED, 128, 64, 2, 2, Y>(p, what, s);
   }
-  return launch_tiled<kFast, GROUPED, GROUPED ? 256 : 128, GROUPED ? 128 : 256, GROUPED ? 4 : 2,
-                      GROUPED ? 2 : 4, Y>(p, what, s);
+  return launch_tiled<kFast, GROUPED, 256, 128, 4, 2, Y>(p, what, s);
 }
 
 }  // namespace

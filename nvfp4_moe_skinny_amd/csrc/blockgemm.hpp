@@ -269,43 +269,52 @@ struct Work {
   int n0;
 };
 
-// Blocks are handed to the eight XCDs in turn (block b to XCD b % 8), each with
-// its own L2, so XCD x gets the consecutive part [x T / 8, (x + 1) T / 8) of
-// the T tiles, in bands of eight row tiles: within a band all row tiles of one
-// column of weight rows, then the next column. The blocks an XCD runs at a time
-// then share row tiles and weight rows about equally, and an expert's weights
-// stay on one XCD or two. The grid has 8 ceil(Tmax / 8) blocks; those past
-// their XCD's part have no rows.
+// The block's tiles. Blocks are handed to the eight XCDs in turn (block b to
+// XCD b % 8), each with its own L2, so XCD x gets the consecutive part
+// [x T / 8, (x + 1) T / 8) of the T tiles, in bands of eight row tiles: within a
+// band all row tiles of one column of weight rows, then the next column. The
+// blocks an XCD runs at a time then share row tiles and weight rows about
+// equally, and an expert's weights stay on one XCD or two. The XCD's blocks
+// take its tiles in turn; a block past its XCD's part has none. T counts at
+// most the tiles that `limit` (the host's bound) allows, whatever off holds.
 template <int BN, int BM, bool GROUPED>
-__device__ __forceinline__ Work block_work(const BlockGemmParams& p, int n_tiles, int lane) {
-  constexpr int kBand = 8;
-  SlotTiles<BM> first;
-  int m_tiles;
-  if constexpr (GROUPED) {
-    first.load(p, 0, lane);
-    m_tiles = count_tiles<BM>(p, first, lane);
-  } else {
-    m_tiles = (p.R + BM - 1) / BM;
+struct BlockTiles {
+  static constexpr int kBand = 8;
+  int m_tiles, n_tiles;
+  uint32_t q, end;
+  // first: the slots 0 .. 255 (grouped; also in next)
+  __device__ __forceinline__ BlockTiles(const BlockGemmParams& p, const SlotTiles<BM>& first,
+                                        int n_tiles, uint32_t limit, int lane)
+      : n_tiles(n_tiles) {
+    if constexpr (GROUPED) {
+      m_tiles = min((uint32_t)count_tiles<BM>(p, first, lane), limit / (uint32_t)n_tiles);
+    } else {
+      m_tiles = (p.R + BM - 1) / BM;
+    }
+    const uint32_t tiles = (uint32_t)m_tiles * (uint32_t)n_tiles;  // at most limit, < 2^31
+    const uint32_t x = blockIdx.x & 7;
+    q = tiles / 8 * x + tiles % 8 * x / 8 + (blockIdx.x >> 3);
+    end = tiles / 8 * (x + 1) + tiles % 8 * (x + 1) / 8;
   }
-  Work w = {{0, 0, 0}, 0};
-  const uint32_t tiles = (uint32_t)m_tiles * (uint32_t)n_tiles;  // at most the grid, < 2^31
-  const uint32_t x = blockIdx.x & 7, i = blockIdx.x >> 3;
-  const uint32_t q0 = tiles / 8 * x + tiles % 8 * x / 8;
-  const uint32_t q1 = tiles / 8 * (x + 1) + tiles % 8 * (x + 1) / 8;
-  const uint32_t q = q0 + i;
-  if (q >= q1) return w;
-  const uint32_t per_band = kBand * (uint32_t)n_tiles;
-  const uint32_t band = q / per_band, in = q - band * per_band;
-  const uint32_t rows = min((uint32_t)kBand, (uint32_t)m_tiles - band * kBand);
-  const uint32_t n = in / rows;
-  const int m = (int)(band * kBand + (in - n * rows));
-  w.n0 = (int)n * BN;
-  if constexpr (GROUPED)
-    w.t = find_tile<BM>(p, first, m, lane);
-  else
-    w.t = {0, m * BM, min(p.R - m * BM, BM)};
-  return w;
-}
+  // The next tile; no rows: there is none.
+  __device__ __forceinline__ Work next(const BlockGemmParams& p, const SlotTiles<BM>& first,
+                                       int lane) {
+    Work w = {{0, 0, 0}, 0};
+    if (q >= end) return w;
+    const uint32_t per_band = kBand * (uint32_t)n_tiles;
+    const uint32_t band = q / per_band, in = q - band * per_band;
+    const uint32_t rows = min((uint32_t)kBand, (uint32_t)m_tiles - band * kBand);
+    const uint32_t n = in / rows;
+    const int m = (int)(band * kBand + (in - n * rows));
+    w.n0 = (int)n * BN;
+    if constexpr (GROUPED)
+      w.t = find_tile<BM>(p, first, m, lane);
+    else
+      w.t = {0, m * BM, min(p.R - m * BM, BM)};
+    q += gridDim.x >> 3;
+    return w;
+  }
+};
 
 // y row of row i of a tile; -1 for rows past the tile's last or a pair index
 // out of range.
@@ -337,13 +346,17 @@ constexpr int kDirectWaves = 4;
 
 template <Mma MODE, bool GROUPED, int NT, int MT, int U, typename Y>
 __global__ void __launch_bounds__(kDirectWaves * 64) direct_gemm_kernel(BlockGemmParams p,
-                                                                        int n_tiles) {
+                                                                        int n_tiles,
+                                                                        uint32_t limit) {
   constexpr int BN = 16 * NT, BM = 16 * MT, W = kDirectWaves;
   constexpr bool FP8 = MODE != Mma::kBf16;
   __shared__ float red[W][BM][BN + 1];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const Work work = block_work<BN, BM, GROUPED>(p, n_tiles, lane);
+  SlotTiles<BM> slots;
+  if constexpr (GROUPED) slots.load(p, 0, lane);
+  const Work work =
+      BlockTiles<BN, BM, GROUPED>(p, slots, n_tiles, limit, lane).next(p, slots, lane);
   const RowTile t = work.t;
   const int n0 = work.n0;
   if (t.rows <= 0) return;
@@ -473,7 +486,7 @@ typedef const __attribute__((address_space(1))) void global_void;
 __device__ __forceinline__ void copy16_to_lds(const uint8_t* src, uint8_t* dst) {
   __builtin_amdgcn_global_load_lds((global_void*)src, (lds_void*)dst, 16, 0, 0);
 }
-__device__ __forceinline__ void copy4_to_lds(const float* src, uint8_t* dst) {
+__device__ __forceinline__ void copy4_to_lds(const void* src, uint8_t* dst) {
   __builtin_amdgcn_global_load_lds((global_void*)src, (lds_void*)dst, 4, 0, 0);
 }
 
@@ -590,15 +603,15 @@ struct Tiled {
     }
   };
 
-  // One step, held by cur. LAST: the last one, which may end past K (k0, k1:
-  // masks of the lane's pieces); otherwise late(i) makes copy i of step k + 1
-  // into the other stage, turn() moves on to step k + 2, early(i) makes its
-  // copies into cur.
+  // One step, held by cur: its products, ahead(i) (copy i of the step two
+  // further on) between them, and the first operands of the next step, held by
+  // other. MASK: the step may end past K (k0, k1: masks of the lane's pieces). LAST:
+  // no step follows, so there are no copies, barrier and first operands.
   // FP8: a tile's block sum is scaled into the result two instructions later,
   // while the matrix cores work on (the scheduling barriers keep that order:
   // left alone, the compiler moves the scaling next to its product and waits
   // there).
-  template <bool LAST, typename Ahead>
+  template <bool MASK, bool LAST, typename Ahead>
   static __device__ __forceinline__ void step(const uint8_t* cur, const uint8_t* other,
                                               const Place& at, First& f, float ws, uint32_t k0,
                                               uint32_t k1, bg_f32x4 (&acc)[NT][MT], Ahead ahead) {
@@ -607,19 +620,19 @@ struct Tiled {
     a[1] = f.a[1];
     Operand<MODE> b[MT];
     float s[MT];
-    if constexpr (LAST) {
+    if constexpr (MASK) {
       mask_frag(a[0], k0, k1);
       mask_frag(a[1], k0, k1);
     }
 #pragma unroll
     for (int j = 0; j < MT; ++j) {
-      if constexpr (LAST) mask_frag(f.b[j], k0, k1);
+      if constexpr (MASK) mask_frag(f.b[j], k0, k1);
       b[j].set(f.b[j]);
       s[j] = f.xs[j] * ws;
     }
     auto weights_ahead = [&](auto row) {
       a[row % 3] = read(cur + at.w + 16 * row * kStepBytes, at.lo);
-      if constexpr (LAST) mask_frag(a[row % 3], k0, k1);
+      if constexpr (MASK) mask_frag(a[row % 3], k0, k1);
     };
     if constexpr (MODE == Mma::kFp8) {
       constexpr int kLag = 3;
@@ -699,145 +712,284 @@ __device__ __forceinline__ void pack4(const bg_f32x4& v, float* dst) {
   *reinterpret_cast<bg_f32x4*>(dst) = v;
 }
 
-template <Mma MODE, bool GROUPED, int BN, int BM, int WVN, int WVM, typename Y>
-__global__ void __launch_bounds__(WVN* WVM * 64, 2)
-    tiled_gemm_kernel(BlockGemmParams p, int n_tiles) {
+template <Mma MODE, bool GROUPED, int BN, int BM, int WVN, int WVM>
+struct TiledLds {
   using T = Tiled<MODE, GROUPED, BN, BM, WVN, WVM>;
-  __shared__ __align__(1024) uint8_t stages[3 * T::kStageBytes];
+  static constexpr int kScaleRows = T::FP8 ? (BN + kBlock8 - 1) / kBlock8 : 0;
+  static constexpr int kScaleBytes = kScaleRows * 256;
+  static constexpr int kPairBytes = GROUPED ? (BM + 63) / 64 * 256 : 0;
+  static constexpr int kPairs = 3 * T::kStageBytes;           // the pairs of three tiles
+  static constexpr int kScales = kPairs + 3 * kPairBytes;     // and 64 weight scales a row
+  static constexpr int kSlots = kScales + 3 * kScaleBytes;
+  static constexpr int kBytes = kSlots + (GROUPED ? 64 * (int)sizeof(SlotTiles<BM>) : 0);
+  // blocks a CU holds: by LDS, and at least 128 registers a lane
+  static constexpr int kPerCu = 160 * 1024 / kBytes < 16 / T::kWaves ? 160 * 1024 / kBytes
+                                                                    : 16 / T::kWaves;
+  static constexpr int kWavesPerSimd = kPerCu * T::kWaves / 4;
+  static_assert(kPerCu >= 1, "fits the LDS");
+};
+
+template <Mma MODE, bool GROUPED, int BN, int BM, int WVN, int WVM, bool MANY, typename Y>
+__global__ void __launch_bounds__(WVN* WVM * 64,
+                                  (TiledLds<MODE, GROUPED, BN, BM, WVN, WVM>::kWavesPerSimd))
+    tiled_gemm_kernel(BlockGemmParams p, int n_tiles, uint32_t limit) {
+  using T = Tiled<MODE, GROUPED, BN, BM, WVN, WVM>;
+  using L = TiledLds<MODE, GROUPED, BN, BM, WVN, WVM>;
+  __shared__ __align__(1024) uint8_t stages[L::kBytes];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const Work work = block_work<BN, BM, GROUPED>(p, n_tiles, lane);
-  const RowTile t = work.t;
-  const int n0 = work.n0;
-  if (t.rows <= 0) return;
+  SlotTiles<BM> slots;
+  if constexpr (GROUPED) slots.load(p, 0, lane);
+  BlockTiles<BN, BM, GROUPED> tiles(p, slots, n_tiles, limit, lane);
+  Work work = tiles.next(p, slots, lane);
+  if (work.t.rows <= 0) return;
 
   const int piece = (lane & 7) ^ (lane >> 3);
   const int wn = (wave % WVN) * T::WN, wm = (wave / WVN) * T::WM;
-  // the weight scales of 64 steps, one a lane
-  const float* wsr = nullptr;
-  float ws_lanes = 1.0f;
-  if constexpr (T::FP8) {
-    wsr = p.ws + ((int64_t)t.e * p.NB + min((n0 + wn) / kBlock8, p.NB - 1)) * p.KB;
-    ws_lanes = wsr[min(lane, p.KB - 1)];
-  }
-  typename T::Cursor c;
-  c.w = p.w + t.e * p.w_mat_bytes + (int64_t)n0 * p.row_bytes;
-  c.x = GROUPED ? p.x : p.x + (int64_t)t.row0 * p.row_bytes;
-  c.xs = p.xs;
-  c.step = 0;
-  c.set_piece(p, piece);
-  typename T::Rows rows;
-#pragma unroll
-  for (int j = 0; j < T::LA; ++j) {
-    const int n = min((j * T::kWaves + wave) * 8 + (lane >> 3), p.N - 1 - n0);
-    rows.a[j] = (uint32_t)n * (uint32_t)p.row_bytes;
-  }
-#pragma unroll
-  for (int j = 0; j < T::LB; ++j) {
-    const int r = (j * T::kWaves + wave) * 8 + (lane >> 3);
-    if constexpr (GROUPED)
-      rows.b[j] = (uint64_t)x_row<GROUPED>(p, t, r) * (uint32_t)p.row_bytes;
-    else
-      rows.b[j] = (uint32_t)min(r, t.rows - 1) * (uint32_t)p.row_bytes;
-  }
-#pragma unroll
-  for (int j = 0; j < T::LS; ++j)
-    rows.s[j] = (uint32_t)x_row<GROUPED>(p, t, wm + 64 * j + (lane & (T::WM < 64 ? T::WM - 1 : 63)));
-
-  bg_f32x4 acc[T::NT][T::MT];
-#pragma unroll
-  for (int i = 0; i < T::NT; ++i)
-#pragma unroll
-    for (int j = 0; j < T::MT; ++j) acc[i][j] = {0.0f, 0.0f, 0.0f, 0.0f};
-
-  // steps 0 and 1, and the first operands of step 0
-  static_for<2>([&](auto q) {
-    static_for<T::kCopies>(
-        [&](auto v) { T::template copy<v>(rows, c, wave, stages + q * T::kStageBytes); });
-    c.advance(p, piece);
-  });
-  // (a use: the wait for this load stays here, instead of one for everything
-  // outstanding in every step)
-  asm volatile("" : "+v"(ws_lanes));
-  arrive<T::kCopies>();
   const typename T::Place at(wave, wn, wm, lane);
-  typename T::First f;
-  f.read_a(stages, at);
-  static_for<T::MT>([&](auto j) { f.template read_b<j>(stages, at); });
-  f.read_xs(stages, at);
+  const bool aligned16 = (p.ldy % (16 / (int)sizeof(Y)) |
+                          (int64_t)((uintptr_t)p.y % 16)) == 0;  // rows of y start on 16 bytes
 
+  // The lane, for what is worked out once a tile: taken out of the loop, as the
+  // compiler would from the plain variable, it holds registers that the products
+  // need, and each reload from scratch would wait for every copy and store.
+  auto lane_here = [&] {
+    int l = lane;
+    asm volatile("" : "+v"(l));
+    return l;
+  };
+  // What a tile's copies need to know before the first one: its pairs and the
+  // first 64 steps' weight scales, one a lane of the first waves; later in LDS.
+  int32_t pair_lane = 0;
+  float scale_lane = 1.0f;
+  auto look_up = [&](const Work& k) {
+    if (k.t.rows <= 0) return;
+    const int l = lane_here();
+    if constexpr (GROUPED)
+      if (wave < (BM + 63) / 64)
+        pair_lane = p.pairs[k.t.row0 + min(wave * 64 + l, k.t.rows - 1)];
+    if constexpr (T::FP8)
+      if (wave < L::kScaleRows)
+        scale_lane = p.ws[((int64_t)k.t.e * p.NB + min(k.n0 / kBlock8 + wave, p.NB - 1)) * p.KB +
+                          min(l, p.KB - 1)];
+  };
+  auto keep_pairs = [&](int third) {
+    const int l = lane_here();
+    if constexpr (GROUPED)
+      if (wave < (BM + 63) / 64)
+        reinterpret_cast<int32_t*>(stages + L::kPairs + third * L::kPairBytes)[wave * 64 + l] =
+            pair_lane;
+  };
+  auto keep_scales = [&](int third) {
+    const int l = lane_here();
+    if constexpr (T::FP8)
+      if (wave < L::kScaleRows)
+        reinterpret_cast<float*>(stages + L::kScales + third * L::kScaleBytes)[wave * 64 + l] =
+            scale_lane;
+  };
+  auto pair = [&](int third, int i) {
+    return reinterpret_cast<const int*>(stages + L::kPairs + third * L::kPairBytes)[i];
+  };
+  auto source_row = [&](const Work& k, int third, int i) -> uint32_t {  // x row of row i
+    if constexpr (!GROUPED) return k.t.row0 + min(i, k.t.rows - 1);
+    const int v = pair(third, i);
+    return (unsigned)v < (unsigned)p.R ? v / p.div : 0;
+  };
+  typename T::Cursor c;
+  typename T::Rows rows;
+  auto enter = [&](const Work& k, int third) {  // the copies go on with this tile
+    const int l = lane_here();
+    c.w = p.w + k.t.e * p.w_mat_bytes + (int64_t)k.n0 * p.row_bytes;
+    c.x = GROUPED ? p.x : p.x + (int64_t)k.t.row0 * p.row_bytes;
+    c.xs = p.xs;
+    c.step = 0;
+    c.set_piece(p, piece);
+#pragma unroll
+    for (int j = 0; j < T::LA; ++j) {
+      const int n = min((j * T::kWaves + wave) * 8 + (l >> 3), p.N - 1 - k.n0);
+      rows.a[j] = (uint32_t)n * (uint32_t)p.row_bytes;
+    }
+#pragma unroll
+    for (int j = 0; j < T::LB; ++j) {
+      const int r = (j * T::kWaves + wave) * 8 + (l >> 3);
+      if constexpr (GROUPED)
+        rows.b[j] = (uint64_t)source_row(k, third, r) * (uint32_t)p.row_bytes;
+      else
+        rows.b[j] = (uint32_t)min(r, k.t.rows - 1) * (uint32_t)p.row_bytes;
+    }
+#pragma unroll
+    for (int j = 0; j < T::LS; ++j)
+      rows.s[j] = source_row(k, third, wm + 64 * j + (l & (T::WM < 64 ? T::WM - 1 : 63)));
+  };
+
+  auto one_more = [&] {
+    const int l = lane_here();
+    SlotTiles<BM> st;
+    if constexpr (GROUPED) __builtin_memcpy(&st, stages + L::kSlots + l * sizeof(st), sizeof(st));
+    return tiles.next(p, st, l);
+  };
+
+  const float* wsr = nullptr;  // the wave's row of weight scales, 64 of them one a lane
+  float ws_lanes = 1.0f;
+  auto scales_of = [&](const Work& k, int third) {
+    if constexpr (T::FP8) {
+      wsr = p.ws + ((int64_t)k.t.e * p.NB + min((k.n0 + wn) / kBlock8, p.NB - 1)) * p.KB;
+      ws_lanes = reinterpret_cast<const float*>(stages + L::kScales + third * L::kScaleBytes +
+                                                wn / kBlock8 * 256)[lane_here()];
+    }
+  };
   auto ws_of = [&](int kb) {
     if (T::FP8 && kb > 0 && (kb & 63) == 0) {
       ws_lanes = wsr[min(kb + lane, p.KB - 1)];
-      asm volatile("" : "+v"(ws_lanes));  // as above
+      // (a use: the wait for this load stays here, instead of one for
+      // everything outstanding in every step)
+      asm volatile("" : "+v"(ws_lanes));
     }
     return T::FP8 ? __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(ws_lanes), kb & 63))
                   : 1.0f;
   };
-  auto step = [&](int kb, const uint8_t* __restrict__ cur, const uint8_t* __restrict__ next,
-                  uint8_t* __restrict__ fill) {
-    T::template step<false>(cur, next, at, f, ws_of(kb), ~0u, ~0u, acc,
-                            [&](auto v) { T::template copy<v>(rows, c, wave, fill); });
+
+  bg_f32x4 acc[T::NT][T::MT];
+  typename T::First f;
+  auto step = [&](auto mask, auto last, int kb, uint32_t k0, uint32_t k1, const uint8_t* __restrict__ cur,
+                  const uint8_t* __restrict__ next, uint8_t* __restrict__ fill) {
+    T::template step<mask, last>(cur, next, at, f, ws_of(kb), k0, k1, acc,
+                           [&](auto v) { T::template copy<v>(rows, c, wave, fill); });
     c.advance(p, piece);
   };
   auto after = [](uint32_t stage) {
     stage += T::kStageBytes;
     return stage == 3 * T::kStageBytes ? 0u : stage;
   };
+  // While a tile's steps run, the next one's pairs and scales are in LDS, and
+  // from the last but one step on its copies are made; the one after that is
+  // looked up in the last step, and put into LDS before the results, where the
+  // wave waits for its copies anyway. With one or two steps a tile starts afresh.
   uint32_t cur = 0, fill = 2 * T::kStageBytes;
-#pragma unroll 1
-  for (int kb = 0; kb + 1 < p.KB; ++kb) {
-    step(kb, stages + cur, stages + after(cur), stages + fill);
-    cur = after(cur);
-    fill = after(fill);
+  auto start = [&](const Work& k, int third) {
+    enter(k, third);
+    cur = 0;
+    fill = 2 * T::kStageBytes;
+    static_for<2>([&](auto q) {
+      static_for<T::kCopies>(
+          [&](auto v) { T::template copy<v>(rows, c, wave, stages + q * T::kStageBytes); });
+      c.advance(p, piece);
+    });
+  };
+  look_up(work);
+  keep_pairs(0);
+  if constexpr (GROUPED) arrive<63>();
+  start(work, 0);
+  keep_scales(0);
+  Work ahead = {{0, 0, 0}, 0}, next = ahead;
+  if constexpr (MANY) ahead = tiles.next(p, slots, lane);
+  if (MANY && ahead.t.rows > 0) {
+    look_up(ahead);
+    keep_pairs(1);
+    keep_scales(1);
+    next = tiles.next(p, slots, lane);
+    // a lane's slots stay in LDS, for the registers are the products'
+    if (GROUPED && wave == 0)
+      __builtin_memcpy(stages + L::kSlots + lane * sizeof(slots), &slots, sizeof(slots));
   }
-  {
-    const int g = lane >> 4, base = (p.KB - 1) * kStepBytes;
-    const uint32_t k0 = base + 16 * g < p.row_bytes ? ~0u : 0u;
-    const uint32_t k1 = base + 64 + 16 * g < p.row_bytes ? ~0u : 0u;
-    T::template step<true>(stages + cur, stages, at, f, ws_of(p.KB - 1), k0, k1, acc, [](auto) {});
-  }
-  arrive<0>();  // the last reads, and copies that nothing needed
-
-  // The results, 16 token rows at a time through the wave's own LDS: a lane
-  // holds four n of one row, and the 16 rows of one store would take 32 bytes
-  // each; read back, eight or more lanes write one row's consecutive 16-byte
-  // pieces.
-  constexpr int kRow = T::WN * (int)sizeof(Y) + 16, kPieces = T::WN * (int)sizeof(Y) / 16;
-  constexpr int kPer = 16 / (int)sizeof(Y);  // elements of a piece
-  static_assert(T::kWaves * 16 * kRow <= 3 * T::kStageBytes, "the exchange fits the stages");
-  uint8_t* ex = stages + wave * 16 * kRow;
-  const bool aligned16 =
-      (p.ldy % kPer | (int64_t)((uintptr_t)p.y % 16)) == 0;  // rows of y start on 16 bytes
-#pragma unroll
-  for (int j = 0; j < T::MT; ++j) {
-    if (wm + 16 * j >= t.rows) break;
+  int third = 0;  // of the looked up
+  bool first = true, flowing = false;  // flowing: the tile's first operands are in registers
+  for (;;) {
+    arrive<63>();  // what was kept is in LDS, and the last results are out of it
+    scales_of(work, third);
+    const int third1 = third == 2 ? 0 : third + 1;
+    if (!flowing) {
+      if (!first) {
+        arrive<0>();  // copies that nothing needed
+        start(work, third);
+      }
+      first = false;
+      arrive<T::kCopies>();
+      f.read_a(stages, at);
+      static_for<T::MT>([&](auto j) { f.template read_b<j>(stages, at); });
+      f.read_xs(stages, at);
+    }
+    flowing = MANY && ahead.t.rows > 0 && p.KB > 2;
 #pragma unroll
     for (int i = 0; i < T::NT; ++i)
-      pack4(acc[i][j], reinterpret_cast<Y*>(ex + (lane & 15) * kRow) + 16 * i + 4 * (lane >> 4));
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
 #pragma unroll
-    for (int q = lane; q < 16 * kPieces; q += 64) {
-      const int r = q / kPieces, piece_n = (q % kPieces) * kPer;
-      const int yr = y_row<GROUPED>(p, t, wm + 16 * j + r);
-      const uint4 v = *reinterpret_cast<const uint4*>(ex + r * kRow + (q % kPieces) * 16);
-      const int n = n0 + wn + piece_n;
-      if (yr < 0 || n >= p.N) continue;
-      Y* dst = static_cast<Y*>(p.y) + yr * p.ldy + n;
-      if (aligned16 && n + kPer <= p.N) {
-        *reinterpret_cast<uint4*>(dst) = v;
-      } else {
-        Y el[kPer];
-        __builtin_memcpy(el, &v, 16);
-#pragma unroll
-        for (int e = 0; e < kPer; ++e)
-          if (n + e < p.N) dst[e] = el[e];
-      }
+      for (int j = 0; j < T::MT; ++j) acc[i][j] = {0.0f, 0.0f, 0.0f, 0.0f};
+    asm volatile("" : "+v"(c.o));  // a use: no wait for a load of it in the loop
+#pragma unroll 1
+    for (int kb = 0; kb + 1 < p.KB; ++kb) {
+      if (flowing && kb + 2 == p.KB) enter(ahead, third1);
+      step(std::false_type{}, std::false_type{}, kb, ~0u, ~0u, stages + cur, stages + after(cur), stages + fill);
+      cur = after(cur);
+      fill = after(fill);
     }
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
+    if constexpr (MANY) look_up(next);
+    {
+      const int g = lane_here() >> 4, base = (p.KB - 1) * kStepBytes;
+      const uint32_t k0 = base + 16 * g < p.row_bytes ? ~0u : 0u;
+      const uint32_t k1 = base + 64 + 16 * g < p.row_bytes ? ~0u : 0u;
+      step(std::true_type{}, std::bool_constant<!MANY>{}, p.KB - 1, k0, k1, stages + cur,
+           stages + after(cur), stages + fill);
+    }
+    Work later = ahead;
+    if constexpr (MANY) {
+      keep_pairs(third1 == 2 ? 0 : third1 + 1);
+      keep_scales(third1 == 2 ? 0 : third1 + 1);
+      later = one_more();
+    } else {
+      arrive<0>();  // the stage's reads are done; also copies that nothing needed
+    }
+
+    // The results, 16 token rows at a time through the wave's part of the stage
+    // that the last step has left: a lane holds four n of one row, and the 16
+    // rows of one store would take 32 bytes each; read back, eight or more lanes
+    // write one row's consecutive 16-byte pieces.
+    constexpr int kRow = T::WN * (int)sizeof(Y) + 16, kPieces = T::WN * (int)sizeof(Y) / 16;
+    constexpr int kPer = 16 / (int)sizeof(Y);  // elements of a piece
+    static_assert(T::kWaves * 16 * kRow <= T::kStageBytes, "the exchange fits a stage");
+    const int l = lane_here();
+    uint8_t* ex = stages + cur + wave * 16 * kRow;
+#pragma unroll
+    for (int j = 0; j < T::MT; ++j) {
+      if (wm + 16 * j >= work.t.rows) break;
+#pragma unroll
+      for (int i = 0; i < T::NT; ++i)
+        pack4(acc[i][j], reinterpret_cast<Y*>(ex + (l & 15) * kRow) + 16 * i + 4 * (l >> 4));
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+#pragma unroll
+      for (int q = l; q < 16 * kPieces; q += 64) {
+        const int r = wm + 16 * j + q / kPieces, n = work.n0 + wn + (q % kPieces) * kPer;
+        const uint4 v =
+            *reinterpret_cast<const uint4*>(ex + q / kPieces * kRow + (q % kPieces) * 16);
+        if (r >= work.t.rows || n >= p.N) continue;
+        int64_t yr = work.t.row0 + r;
+        if constexpr (GROUPED) {
+          yr = pair(third, r);
+          if ((uint64_t)yr >= (uint64_t)p.R) continue;
+        }
+        Y* dst = static_cast<Y*>(p.y) + yr * p.ldy + n;
+        if (aligned16 && n + kPer <= p.N) {
+          *reinterpret_cast<uint4*>(dst) = v;
+        } else {
+          Y el[kPer];
+          __builtin_memcpy(el, &v, 16);
+#pragma unroll
+          for (int e = 0; e < kPer; ++e)
+            if (n + e < p.N) dst[e] = el[e];
+        }
+      }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+    }
+    if (!MANY || ahead.t.rows <= 0) break;
+    cur = after(cur);
+    fill = after(fill);
+    work = ahead;
+    ahead = next;
+    next = later;
+    third = third1;
   }
+  if constexpr (MANY) arrive<0>();  // copies that nothing needed
 }
 
 }  // namespace nvfp4moe
