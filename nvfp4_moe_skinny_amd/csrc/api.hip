@@ -787,56 +787,65 @@ template <Mma MODE, bool GROUPED, int BN, int BM, int WVN, int WVM, typename Y>
 int32_t launch_tiled(const BlockGemmParams& p, const char* what, hipStream_t s) {
   const int64_t tiles = block_gemm_tiles(p, GROUPED, BN, BM);
   if (tiles > kMaxGrid) return grid_too_large(what);
-  // a CU's worth of blocks for each of the 256 CUs, which share the tiles out
-  const int64_t fill = 256 * TiledLds<MODE, GROUPED, BN, BM, WVN, WVM>::kPerCu;
+  // a CU's worth of blocks for each of the 256 CUs; more tiles than that are
+  // shared out among those blocks
+  constexpr int64_t fill = 256 * TiledLds<MODE, GROUPED, BN, BM, WVN, WVM>::kPerCu;
   const dim3 block(WVN * WVM * 64);
   const int n_tiles = (p.N + BN - 1) / BN;
-  if (tiles <= fill)
-    hipLaunchKernelGGL((tiled_gemm_kernel<MODE, GROUPED, BN, BM, WVN, WVM, false, Y>),
-                       dim3((unsigned)((tiles + 7) / 8 * 8)), block, 0, s, p, n_tiles,
-                       (uint32_t)tiles);
-  else
-    hipLaunchKernelGGL((tiled_gemm_kernel<MODE, GROUPED, BN, BM, WVN, WVM, true, Y>),
-                       dim3((unsigned)fill), block, 0, s, p, n_tiles, (uint32_t)tiles);
+  if constexpr (BN > 64) {  // (the 64 x 64 tiles of kSmallTiles fit at once)
+    if (tiles > fill) {
+      hipLaunchKernelGGL((tiled_gemm_kernel<MODE, GROUPED, BN, BM, WVN, WVM, true, Y>), dim3(fill),
+                         block, 0, s, p, n_tiles, (uint32_t)tiles);
+      return launched(what);
+    }
+  }
+  hipLaunchKernelGGL((tiled_gemm_kernel<MODE, GROUPED, BN, BM, WVN, WVM, false, Y>),
+                     dim3((unsigned)((tiles + 7) / 8 * 8)), block, 0, s, p, n_tiles,
+                     (uint32_t)tiles);
   return launched(what);
 }
 
 int64_t tiles_of(int64_t n, int64_t per) { return (n + per - 1) / per; }
 
 // Which kernel and tile: few blocks need many short ones to fill the chip,
-// many rows need large tiles (fewer bytes through L2 per product). The
+// many rows need large tiles (fewer bytes through L2 and LDS per product). The
 // thresholds are crossovers measured on an MI355X (us, FP8 -> BF16 unless
-// noted; weights cycled through more than the Infinity Cache):
-//   dense    N = 5120, K = 2048
-//     M = 1         direct 5.5, 128x32 tiles 11 (FP32 result)
-//     M = 32        direct 8.8 (640 blocks), 64x64 8.1;  M = 64: 13, 7.6
-//     M = 24, N = 1000, K = 4096   direct 6.7 (126 blocks), 64x64 19 (FP32 result)
-//     M = 512       64x64 13.6 (640 blocks), 128x64 13.4;  M = 2048: 45, 37
-//     M = 2048      128x64 37.4 (1280 blocks), 256x128 39.5;  M = 8192: 131, 107
-//   grouped  E = 256, k = 8, gate_up 2048 -> 1024
-//     M = 1         direct 6.0, 128x32 12.7 (FP32 result);  M = 4: 16.8, 14.0
-//     M = 256       128x32 96 (8 rows a slot), 128x64 98;  M = 1024 (32): 121, 108
-//     M = 1024      128x64 108, 256x128 119;  M = 512, E = 64 (64): 42, 33
-//     M = 256, E = 8, k = 2        64x64 11.2 (128 blocks), 256x128 21
+// noted; weights cycled through more than the Infinity Cache), beside each rule
+// the two sides of it:
+//   direct, dense, at most 640 blocks of 16 x 16
+//     N = 5120, K = 2048, M = 16 (320 blocks) direct 7.0, 64x64 8.4;  M = 32
+//     (640): 8.9, 8.6;  M = 64: 12.6, 8.7
+//   direct, grouped, at most 1024 blocks and 8 rows a slot (2048 -> 1024, k = 8)
+//     M = 2 (1024 blocks) 10.2, 128x32 10.9;  M = 4: 18.2, 13.3;  E = 8, k = 2,
+//     M = 16 (512): 8.0, 64x64 11.4;  M = 256: 27, 12.4
+//   64x64, at most 256 tiles (one a CU)
+//     M = 192 (240 tiles) 9.1, 128x64 10.6;  M = 256 (320): 11.1, 10.8;
+//     grouped E = 8, M = 1024 (512): 23.3, 18.4
+//   128x32, at most 32 rows (grouped: 16 a slot, which scatter about their mean)
+//     N = 32768, M = 32  14.6, 128x64 15.6;  E = 256, M = 64 (2 a slot): 90.8,
+//     91.3;  M = 512 (16): 101.2, 101.4;  M = 1024 (32): 131, 109
+//   128x64, at most 512 tiles (two a CU), or grouped with less than 48 rows a slot
+//     M = 512 (320 tiles) 14.4, 256x128 17.9;  M = 1024 (640): 23.7, 19.7;
+//     E = 64, k = 8, M = 256 (32 a slot): 28.9, 32.2;  M = 512 (64): 37.3, 33.1
+//   128x64 for all the rest, codes decoded (FP32 result)
+//     M = 2048  54.1, 256x128 62.8;  grouped E = 64, M = 512: 41.7, 42.6
 template <bool FP8, bool GROUPED, typename Y>
 int32_t launch_block_gemm(const BlockGemmParams& p, const char* what, hipStream_t s) {
   constexpr Mma kExact = FP8 ? Mma::kFp8Exact : Mma::kBf16;
   constexpr Mma kFast = FP8 && sizeof(Y) == 2 ? Mma::kFp8 : kExact;
+  constexpr int64_t kSmallTiles = 256, kMidTiles = 512;
   const int64_t per_slot = tiles_of(p.R, p.slots);  // mean rows of a slot (dense: all)
-  const int64_t direct = p.slots * tiles_of(per_slot, 16) * tiles_of(p.N, 16);
-  const int64_t small = p.slots * tiles_of(per_slot, 64) * tiles_of(p.N, 64);
-  if constexpr (GROUPED) {
-    if (per_slot <= 8 && direct <= 1024) return launch_direct<kExact, GROUPED, Y>(p, what, s);
-    if (per_slot <= 16) return launch_tiled<kFast, GROUPED, 128, 32, 4, 1, Y>(p, what, s);
-    if (small <= 640) return launch_tiled<kFast, GROUPED, 64, 64, 2, 2, Y>(p, what, s);
-    if (per_slot < 48) return launch_tiled<kFast, GROUPED, 128, 64, 2, 2, Y>(p, what, s);
-  } else {
-    if (direct <= 640) return launch_direct<kExact, GROUPED, Y>(p, what, s);
-    if (p.R <= 32) return launch_tiled<kFast, GROUPED, 128, 32, 4, 1, Y>(p, what, s);
-    if (small <= 640) return launch_tiled<kFast, GROUPED, 64, 64, 2, 2, Y>(p, what, s);
-    if (small <= 2560) return launch_tiled<kFast, GROUPED, 128, 64, 2, 2, Y>(p, what, s);
-  }
-  return launch_tiled<kFast, GROUPED, 256, 128, 4, 2, Y>(p, what, s);
+  auto tiles = [&](int n, int m) { return p.slots * tiles_of(per_slot, m) * tiles_of(p.N, n); };
+  if (tiles(16, 16) <= (GROUPED ? 1024 : 640) && !(GROUPED && per_slot > 8))
+    return launch_direct<kExact, GROUPED, Y>(p, what, s);
+  if (tiles(64, 64) <= kSmallTiles)
+    return launch_tiled<kFast, GROUPED, 64, 64, 2, 2, Y>(p, what, s);
+  if (per_slot <= (GROUPED ? 16 : 32))
+    return launch_tiled<kFast, GROUPED, 128, 32, 4, 1, Y>(p, what, s);
+  if constexpr (kFast != Mma::kFp8Exact)
+    if (tiles(128, 64) > kMidTiles && !(GROUPED && per_slot < 48))
+      return launch_tiled<kFast, GROUPED, 256, 128, 4, 2, Y>(p, what, s);
+  return launch_tiled<kFast, GROUPED, 128, 64, 2, 2, Y>(p, what, s);
 }
 
 }  // namespace

@@ -452,7 +452,7 @@ __global__ void __launch_bounds__(kDirectWaves * 64) direct_gemm_kernel(BlockGem
 
 // ---- many rows: operands staged in LDS --------------------------------------------------
 //
-// One block per (row tile of BM rows, BN weight rows), wave tiles of
+// A block multiplies tiles of BM rows and BN weight rows, wave tiles of
 // BN / WVN x BM / WVM. A k step of the BN + BM rows (128 bytes each, and the x
 // scales) is copied to one of three LDS stages by direct loads, 16 bytes a
 // lane, two steps ahead of its products. Piece c of row r lies at piece
@@ -469,16 +469,25 @@ __global__ void __launch_bounds__(kDirectWaves * 64) direct_gemm_kernel(BlockGem
 // reads this stage any more; during the last row the first operands of step
 // k + 1 replace those just used. So the matrix cores have work across the
 // barrier (with the barrier between the steps and the operands read after it:
-// grouped gate_up 2048 -> 1024 at M = 4 15.0 us, this way 13.2), and a copy has
+// grouped gate_up 2048 -> 1024 at M = 4 15.0 us, this way 13.0), and a copy has
 // more than a step to arrive (with two stages and one step: M = 16 53 us,
 // this way 44; more than three stages only cost blocks per CU).
 //
-// What bounds large products (M = 8192, 2048 -> 5120: 95 us, 1.8 PFLOP/s): the
-// products and scalings alone run at about 2.8 PFLOP/s (K = 8192; matrix
-// instructions and scalings without operands at 4.0, at the clock of about
-// 2 GHz that the chip holds under them); the copies into LDS beside the
-// operand reads cost the rest (a 1 KB direct load about 24 clocks of the LDS, a
-// 1 KB read 4; through registers and LDS stores it took the same time).
+// With more tiles than the chip holds at once (MANY), a CU's worth of blocks
+// takes them in turn: the last two steps of a tile copy the first two of the
+// next one, whose pairs and scales were looked up a tile earlier, so only the
+// results stand between two tiles (one tile a block: M = 8192, 2048 -> 5120
+// 98.6 us, this way 93.6; grouped gate_up, E = 256, M = 8192 265 and 241).
+//
+// What bounds large products (93.6 us, 1.84 PFLOP/s): LDS. A 256 x 128 step is
+// 48 direct loads of 1 KB, about 24 clocks of the LDS each beside reads, and
+// 128 KB of operand reads at about 230 bytes a clock, 0.86 us of the step's 1.1;
+// its matrix instructions alone take 0.67 (through registers and LDS stores it
+// took the same time; 256 x 256 tiles have a third fewer bytes, but only two
+// stages fit: 93.7 with one tile a block). Grouped products read their weights
+// from HBM beside that (241 us: 2.9 TB/s, and rows that end inside a tile cost a
+// quarter of the products); with few rows a slot those bytes are the bound
+// (M = 256 98 us, 5.5 TB/s).
 typedef __attribute__((address_space(3))) void lds_void;
 typedef const __attribute__((address_space(1))) void global_void;
 
