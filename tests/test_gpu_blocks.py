@@ -199,6 +199,26 @@ def test_block_gemm_integers_exact(m, gpu, M, N, K):
     assert torch.equal(m.fp8_block_gemm(xd, wd).cpu(), r.to(torch.bfloat16))
 
 
+@pytest.mark.parametrize("K", [16, 144, 272, 400, 8320])
+@pytest.mark.parametrize("M,N", [(2176, 4112), (2300, 4000), (5000, 1300)])
+def test_block_gemm_more_tiles_than_blocks(m, gpu, M, N, K):
+    """Blocks that take several tiles in turn, with one to four k steps and with
+    more than 64: integers up to 4 (8320 products of at most 16: exact in FP32)."""
+    g = torch.Generator(device=gpu).manual_seed(M + N + K)
+    u8 = lambda t: t.to(torch.float8_e4m3fn).view(torch.uint8)
+    ints = lambda *s: torch.randint(-4, 5, s, generator=g, device=gpu).float()
+    p2 = lambda *s: 2.0 ** torch.randint(0, 2, s, generator=g, device=gpu).float()
+    x = m.Fp8Rows(u8(ints(M, K)), p2(ref.nblk(K), M))
+    w = m.Fp8Blocks(u8(ints(1, N, K)), p2(1, ref.nblk(N), ref.nblk(K)))
+    want = torch.mm(ref.dequant_rows(x).to(gpu), ref.dequant_blocks(w)[0].to(gpu).t().contiguous())
+    assert want.abs().max() < 2 ** 24
+    out = torch.full((M + 1, N + 3), 7.0, dtype=torch.bfloat16, device=gpu)
+    m.fp8_block_gemm(x, w, out=out[:M, :N])
+    assert torch.equal(out[:M, :N], want.to(torch.bfloat16))
+    assert (out[M] == 7.0).all() and (out[:, N:] == 7.0).all()
+    assert torch.equal(m.fp8_block_gemm(x, w, out_dtype=torch.float32).double(), want)
+
+
 def test_block_gemm_nan_codes_stay_in_their_row_and_column(m, gpu):
     for M, N, K in ((5, 70, 272), (300, 400, 272)):
         x, w = _quantized(m, gpu, 9, M, N, K)

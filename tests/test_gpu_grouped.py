@@ -94,6 +94,37 @@ def test_grouped_integers_exact(m, gpu, typ, M, N, K):
 
 
 @pytest.mark.parametrize("typ", ["fp8", "bf16"])
+@pytest.mark.parametrize("K", [16, 144, 272, 400])
+@pytest.mark.parametrize("M,E,k,N,how", [
+    (600, 300, 4, 260, "even"), (1500, 200, 4, 260, "skewed"), (2000, 40, 4, 520, "even"),
+    (4000, 300, 4, 260, "skewed")])
+def test_grouped_more_tiles_than_blocks(m, gpu, typ, K, M, E, k, N, how):
+    """Blocks that take several tiles in turn, of every tile shape, with one k
+    step and more, up to 300 slots (a wave holds 256 at a time): exact integers."""
+    g = torch.Generator(device=gpu).manual_seed(M + N + K)
+    ints = lambda *s: torch.randint(-4, 5, s, generator=g, device=gpu).float()
+    p2 = lambda *s: 2.0 ** torch.randint(0, 3, s, generator=g, device=gpu).float()
+    ids = _ids(M, M, E, k, how)
+    r = ref.routing_of(m, ids, E, gpu)
+    if typ == "fp8":
+        u8 = lambda t: t.to(torch.float8_e4m3fn).view(torch.uint8)
+        x = m.Fp8Rows(u8(ints(M, K)), p2(ref.nblk(K), M))
+        w = m.Fp8Blocks(u8(ints(E, N, K)), p2(E, ref.nblk(N), ref.nblk(K)))
+        x64, w64 = ref.dequant_rows(x).to(gpu), ref.dequant_blocks(w).to(gpu)
+    else:
+        x, w = ints(M, K).to(torch.bfloat16), ints(E, N, K).to(torch.bfloat16)
+        x64, w64 = x.double(), w.double()
+    want = torch.empty((M * k, N), dtype=torch.float64, device=gpu)
+    flat = ids.reshape(-1).to(gpu)
+    for e in range(E):
+        p = (flat == e).nonzero().reshape(-1)
+        want[p] = torch.mm(x64[p // k], w64[e].t().contiguous())
+    assert want.abs().max() < 2 ** 24
+    assert torch.equal(m.moe_grouped_gemm(x, r, w, out_dtype=torch.float32).double(), want)
+    assert torch.equal(m.moe_grouped_gemm(x, r, w), want.to(torch.bfloat16))
+
+
+@pytest.mark.parametrize("typ", ["fp8", "bf16"])
 @pytest.mark.parametrize("M", [6, 400])
 def test_grouped_local_experts_only(m, gpu, typ, M):
     """A rank that passes some experts' slots: other pairs' rows stay as they
