@@ -382,7 +382,9 @@ typedef struct moe_grouped_args {
  * R * N <= 2^38. The grouping
  * arrays are read on the device: only the first min(n_active, E, R) slots
  * count; slot s takes positions active_offsets[s] to active_offsets[s + 1] of
- * pairs and expert active[s]. Rows of y whose pair no such slot holds are left
+ * pairs and expert active[s]. Offsets outside [0, R] count as the nearer end,
+ * and a slot whose end is not behind its start is empty; where slots overlap,
+ * which of their rows are written is not defined. Rows of y whose pair no such slot holds are left
  * as they were (a rank that holds some of the experts passes their slots
  * only); a pair outside [0, R) or an expert outside [0, E) is skipped. A pair
  * that appears twice is written twice, in either order. One launch. */

@@ -162,6 +162,44 @@ def test_grouped_local_experts_only(m, gpu, typ, M):
     assert (m.moe_grouped_gemm(x, r2, w, out_dtype=torch.float32, out=out) == 5.0).all()
 
 
+@pytest.mark.parametrize("typ", ["fp8", "bf16"])
+@pytest.mark.parametrize("M", [2, 60, 3000])
+def test_grouped_offsets_out_of_order(m, gpu, typ, M):
+    """Offsets and counts outside their range are taken as the nearer end, a slot
+    that ends before it starts is empty; rows around y stay as they were."""
+    E, k, N, K = 9, 2, 260, 272
+    ids = _ids(M, M, E, k, "even")
+    r = ref.routing_of(m, ids, E, gpu)
+    x, w, x64, w64 = _operands(m, gpu, M, typ, M, E, N, K)
+    R, half = M * k, M * k // 2
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device=gpu)
+    pairs = torch.randperm(R, generator=torch.Generator().manual_seed(M)).int().to(gpu)
+    big = 2 ** 31 - 1
+    # slot 0: [0, half) of expert 3; 1: empty; 2: [0, 0) after the clamp; 3: empty;
+    # 4: [half, R) of expert 5; 5: [R, R); the others end before they start
+    off = i32(-7, half, 0, -big, half, big, R + 1, half, 0, -1)
+    active = i32(3, 4, 6, 7, 5, 1, 2, 8, 0)
+    # slot 3 would be [0, half) as well: an expert that does not exist drops it
+    active[3] = -2
+    r2 = m.Routing(r.ids, r.w, r.counts, r.offsets, pairs, active, off, i32(big))
+    buf = torch.full((R + 2, N + 8), 5.0, device=gpu)
+    m.moe_grouped_gemm(x, r2, w, out_dtype=torch.float32, out=buf[1:-1, :N])
+    torch.cuda.synchronize()
+    y = buf.cpu().double()
+    assert (y[0] == 5.0).all() and (y[-1] == 5.0).all() and (y[:, N:] == 5.0).all()
+    p = pairs.cpu().long()
+    for part, slot, e in ((p[:half], 0, 3), (p[half:], 4, 5)):
+        if slot >= min(E, R):  # (four pairs have at most four slots)
+            assert (y[1:-1, :N][part] == 5.0).all()
+            continue
+        want, mag = ref.gemm_f64(x64[part // k], w64[e])
+        ref.assert_close(y[1:-1, :N][part], want, ref.gemm_tol(want, mag, K, False))
+    r2.n_active.fill_(-big)
+    buf.fill_(5.0)
+    m.moe_grouped_gemm(x, r2, w, out_dtype=torch.float32, out=buf[1:-1, :N])
+    assert (buf == 5.0).all()
+
+
 @pytest.mark.parametrize("M", [3, 300])
 def test_grouped_bf16_infinity_and_nan(m, gpu, M):
     """An infinite or NaN weight reaches its own column of its own expert only;
