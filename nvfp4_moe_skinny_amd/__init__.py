@@ -525,11 +525,14 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
 def _elsewhere(t: torch.Tensor, stream) -> bool:
     """Whether a call on t has to enter another device or stream first (_on)."""
     if not t.is_cuda:
         raise ValueError("expected a GPU tensor")
-    return stream is not None or t.get_device() != torch.cuda.current_device()
+    return stream is not None or t.get_device() != _current_device()
 
 
 def _on(t: torch.Tensor, stream):
@@ -598,13 +601,13 @@ def fp8_quantize_rows(x: torch.Tensor, swiglu: bool = False, stream=None,
     xt = _float_type(x.dtype, "x")
     _check_rows(x, "x")
     M, K = x.shape
-    ldx = _row_stride(x)
+    ldx = x.stride(0) if M > 1 else K
     if swiglu:
         K //= 2
     if out is None:
         dev = x.device
-        out = Fp8Rows(torch.empty((M, K), dtype=torch.uint8, device=dev),
-                      torch.empty((_blocks128(K), M), dtype=torch.float32, device=dev))
+        out = Fp8Rows(torch.empty(M, K, dtype=torch.uint8, device=dev),
+                      torch.empty(_blocks128(K), M, dtype=torch.float32, device=dev))
     else:
         _want(out.codes, "out.codes", (M, K), torch.uint8, x.device)
         _want(out.scales, "out.scales", (_blocks128(K), M), torch.float32, x.device)
@@ -628,8 +631,8 @@ def fp8_quantize_blocks(w: torch.Tensor, stream=None,
     G, N, K = w.shape
     dev = w.device
     if out is None:
-        out = Fp8Blocks(torch.empty((G, N, K), dtype=torch.uint8, device=dev),
-                        torch.empty((G, _blocks128(N), _blocks128(K)), dtype=torch.float32,
+        out = Fp8Blocks(torch.empty(G, N, K, dtype=torch.uint8, device=dev),
+                        torch.empty(G, _blocks128(N), _blocks128(K), dtype=torch.float32,
                                     device=dev))
     else:
         _want(out.codes, "out.codes", (G, N, K), torch.uint8, dev)
@@ -653,7 +656,7 @@ def fp8_block_gemm(x: Fp8Rows, w: Fp8Blocks, out_dtype: torch.dtype = torch.bflo
         raise ValueError("w must hold one matrix")
     yt = _float_type(out_dtype, "out_dtype")
     if out is None:
-        out = torch.empty((M, N), dtype=out_dtype, device=dev)
+        out = torch.empty(M, N, dtype=out_dtype, device=dev)
         ldy = N
     else:
         _want_rows(out, "out", (M, N), out_dtype, dev)
@@ -707,7 +710,7 @@ def moe_grouped_gemm(x, routing: Routing, w, out_dtype: torch.dtype = torch.bflo
     a.E, a.N, a.K = E, N, K
     a.y_type = _float_type(out_dtype, "out_dtype")
     if out is None:
-        out = torch.empty((R, N), dtype=out_dtype, device=dev)
+        out = torch.empty(R, N, dtype=out_dtype, device=dev)
         a.ldy = N
     else:
         _want_rows(out, "out", (R, N), out_dtype, dev)
@@ -737,7 +740,7 @@ def moe_combine(y: torch.Tensor, w: torch.Tensor, shared: Optional[torch.Tensor]
     _want(shared, "shared", (M, H), y.dtype, dev)
     _want(residual, "residual", (M, H), torch.bfloat16, dev)
     if out is None:
-        out = torch.empty((M, H), dtype=torch.bfloat16, device=dev)
+        out = torch.empty(M, H, dtype=torch.bfloat16, device=dev)
     else:
         _want(out, "out", (M, H), torch.bfloat16, dev)
     _check(lib.moe_combine(y.data_ptr(), yt, w.data_ptr(),
