@@ -772,14 +772,23 @@ int32_t grid_too_large(const char* what) {
   return fail(NVFP4MOE_ERR_UNSUPPORTED, "%s: more tiles than a grid holds", what);
 }
 
+// U steps are requested at a time by each of the four waves, also those past
+// the last: with few steps one at a time is enough and asks for less (M = 1 us,
+// FP8 K -> 5120 unless noted, grouped: eight experts -> 2048; U = 1, 2, 4:
+//   K = 512 (4 steps)  3.4, 4.0, 5.1;   K = 1024 (8)  4.4, 4.1, 5.2
+//   grouped K = 1280 (10)  6.9, 7.4, 8.8;   M = 8, K = 1536 (12)  5.5, 6.2, 6.2
+//   K = 1664 (13)  5.9, 5.6, 5.6;   K = 2048 (16)  6.0, 5.6, 5.6
+//   K = 2304 (18)  6.8, 6.5, 7.2;   N = 2048, K = 4096 (32)  8.1, 6.5, 5.8).
 template <Mma MODE, bool GROUPED, typename Y>
 int32_t launch_direct(const BlockGemmParams& p, const char* what, hipStream_t s) {
-  constexpr int NT = 1, MT = 1, U = 4;
+  constexpr int NT = 1, MT = 1;
   const int64_t tiles = block_gemm_tiles(p, GROUPED, 16 * NT, 16 * MT);
   if (tiles > kMaxGrid - 7) return grid_too_large(what);
-  hipLaunchKernelGGL((direct_gemm_kernel<MODE, GROUPED, NT, MT, U, Y>),
-                     dim3((unsigned)((tiles + 7) / 8 * 8)), dim3(kDirectWaves * 64), 0, s, p,
-                     (p.N + 16 * NT - 1) / (16 * NT), (uint32_t)tiles);
+  const auto kernel = p.KB <= 12   ? direct_gemm_kernel<MODE, GROUPED, NT, MT, 1, Y>
+                      : p.KB <= 24 ? direct_gemm_kernel<MODE, GROUPED, NT, MT, 2, Y>
+                                   : direct_gemm_kernel<MODE, GROUPED, NT, MT, 4, Y>;
+  hipLaunchKernelGGL(kernel, dim3((unsigned)((tiles + 7) / 8 * 8)), dim3(kDirectWaves * 64), 0, s,
+                     p, (p.N + 16 * NT - 1) / (16 * NT), (uint32_t)tiles);
   return launched(what);
 }
 

@@ -86,8 +86,12 @@ __device__ __forceinline__ float silu_mul(float a, float b) { return a / (1.0f +
 
 constexpr int kQuantRowsThreads = 256;
 
-// One 128-block per 16 lanes, eight elements per lane; a block of 256 threads
-// takes 16 consecutive blocks of the row-major order.
+// One 128-block per 16 lanes, eight elements per lane (16 bytes of BF16), held
+// in registers between the maximum, found by row rotations among the 16 lanes,
+// and the codes: one pass over the data, no LDS, no barrier. A block of 256
+// threads takes 16 consecutive blocks of the row-major order. Bound: memory for
+// many rows (swiglu, M = 8192, K = 512, 21 MB: 7.8 us, 2.7 TB/s, of which a
+// launch and one round trip take 2.2, the time of M = 4).
 template <typename T, bool SWIGLU>
 __global__ void __launch_bounds__(kQuantRowsThreads) fp8_quantize_rows_kernel(
     const T* __restrict__ x, int64_t M, int K, int64_t ldx, int KB, uint8_t* __restrict__ codes,
@@ -125,7 +129,9 @@ __global__ void __launch_bounds__(kQuantRowsThreads) fp8_quantize_rows_kernel(
 constexpr int kQuantBlocksThreads = 256;
 
 // One 128 x 128 block per workgroup: 16 lanes per row, 16 rows at a time, the
-// block held in registers between the maximum and the codes.
+// block held in registers between the maximum and the codes, so each element is
+// read once. Bound: memory (256 x [1024][2048] BF16, 1.6 GB: 298 us, 5.4 TB/s;
+// [2048][4096], 25 MB: 6.6 us).
 template <typename T>
 __global__ void __launch_bounds__(kQuantBlocksThreads) fp8_quantize_blocks_kernel(
     const T* __restrict__ x, int64_t N, int K, int NB, int KB, uint8_t* __restrict__ codes,

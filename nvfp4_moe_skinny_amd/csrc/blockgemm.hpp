@@ -342,6 +342,11 @@ __device__ __forceinline__ void store_y(float* y, float v) { *y = v; }
 //
 // One block per (row tile of 16 MT rows, 16 NT weight rows); wave v takes k
 // steps v, v + W, ... and the W partial tiles are added in LDS in wave order.
+// Bound: the latency of one read of the weights (M = 1, 2048 -> 5120, 10.5 MB:
+// 5.6 us, 1.9 TB/s, of which a launch with nothing to read takes 2; 2048 -> 1024
+// of eight experts, 16.8 MB: 6.5 us, 2.6 TB/s), so the chip needs many short
+// blocks: 16 weight rows a block (32: 5.8 us, and 8.5 against 5.8 at N = 2048,
+// K = 4096), four waves (eight: 5.6, with 16.8 MB 7.0 against 6.5).
 constexpr int kDirectWaves = 4;
 
 template <Mma MODE, bool GROUPED, int NT, int MT, int U, typename Y>

@@ -3,7 +3,9 @@
 // in j order, then the shared term, then the residual, FP32, one rounding at
 // the end. A pair of weight 0 adds nothing, whatever its y row holds (a pair
 // whose expert lives elsewhere has no y).
-// Bound: memory (k y rows read per row written).
+// Bound: memory (k y rows read per row written; M = 4096, k = 8, H = 2048, BF16,
+// 168 MB: 30 us, 5.5 TB/s; M = 16 in FP32, 1.3 MB: 3.2 us, a launch and one round
+// trip). Four outputs a thread, 8 or 16 bytes a load, all k loads in flight.
 #pragma once
 
 #include "common.hpp"
