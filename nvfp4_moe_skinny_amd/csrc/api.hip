@@ -792,23 +792,23 @@ int32_t launch_direct(const BlockGemmParams& p, const char* what, hipStream_t s)
   return launched(what);
 }
 
-template <Mma MODE, bool GROUPED, int BN, int BM, int WVN, int WVM, typename Y>
+template <Mma MODE, bool GROUPED, int BN, int BM, int WVN, int WVM, int S, typename Y>
 int32_t launch_tiled(const BlockGemmParams& p, const char* what, hipStream_t s) {
   const int64_t tiles = block_gemm_tiles(p, GROUPED, BN, BM);
   if (tiles > kMaxGrid) return grid_too_large(what);
-  // a CU's worth of blocks for each of the 256 CUs; more tiles than that are
-  // shared out among those blocks
-  constexpr int64_t fill = 256 * TiledLds<MODE, GROUPED, BN, BM, WVN, WVM>::kPerCu;
   const dim3 block(WVN * WVM * 64);
   const int n_tiles = (p.N + BN - 1) / BN;
-  if constexpr (BN > 64) {  // (the 64 x 64 tiles of kSmallTiles fit at once)
+  // a CU's worth of blocks for each of the 256 CUs; more tiles than that are
+  // shared out among those blocks (tiles with four stages are used where they fit)
+  constexpr int64_t fill = 256 * TiledLds<MODE, GROUPED, BN, BM, WVN, WVM, S>::kPerCu;
+  if constexpr (S == 3) {
     if (tiles > fill) {
-      hipLaunchKernelGGL((tiled_gemm_kernel<MODE, GROUPED, BN, BM, WVN, WVM, true, Y>), dim3(fill),
-                         block, 0, s, p, n_tiles, (uint32_t)tiles);
+      hipLaunchKernelGGL((tiled_gemm_kernel<MODE, GROUPED, BN, BM, WVN, WVM, S, true, Y>),
+                         dim3(fill), block, 0, s, p, n_tiles, (uint32_t)tiles);
       return launched(what);
     }
   }
-  hipLaunchKernelGGL((tiled_gemm_kernel<MODE, GROUPED, BN, BM, WVN, WVM, false, Y>),
+  hipLaunchKernelGGL((tiled_gemm_kernel<MODE, GROUPED, BN, BM, WVN, WVM, S, false, Y>),
                      dim3((unsigned)((tiles + 7) / 8 * 8)), block, 0, s, p, n_tiles,
                      (uint32_t)tiles);
   return launched(what);
@@ -821,17 +821,25 @@ int64_t tiles_of(int64_t n, int64_t per) { return (n + per - 1) / per; }
 // thresholds are crossovers measured on an MI355X (us, FP8 -> BF16 unless
 // noted; weights cycled through more than the Infinity Cache), beside each rule
 // the two sides of it:
-//   direct, dense, at most 640 blocks of 16 x 16
-//     N = 5120, K = 2048, M = 16 (320 blocks) direct 7.0, 64x64 8.4;  M = 32
-//     (640): 8.9, 8.6;  M = 64: 12.6, 8.7
-//   direct, grouped, at most 1024 blocks and 8 rows a slot (2048 -> 1024, k = 8)
-//     M = 2 (1024 blocks) 10.2, 128x32 10.9;  M = 4: 18.2, 13.3;  E = 8, k = 2,
-//     M = 16 (512): 8.0, 64x64 11.4;  M = 256: 27, 12.4
-//   64x64, at most 256 tiles (one a CU)
-//     M = 192 (240 tiles) 9.1, 128x64 10.6;  M = 256 (320): 11.1, 10.8;
+//   direct, at most 512 blocks of 16 x 16, grouped at most 8 rows a slot
+//     N = 8192, K = 2048, M = 16 (512 blocks) direct 7.0, 64x32 7.8;  N = 5120,
+//     M = 17 (640): 8.8, 6.9;  N = 16384, M = 4 (1024): 9.1, 8.8
+//     grouped 2048 -> 1024, k = 8, M = 1 (512 blocks) 6.4, 64x32 8.2;  M = 2
+//     (1024): 9.7, 9.2;  E = 8, k = 2, M = 32 (8 a slot): 8.1, 8.8;  M = 64 (16):
+//     11.4, 8.9
+//   with codes decoded (FP32 result) 1024 blocks, at most 16 rows a slot
+//     M = 4, N = 16384 (1024) 9.2, 10.1;  M = 17, N = 5120: 8.9, 8.7;  grouped
+//     M = 2 (1024): 9.8, 11.1;  M = 4: 16.7, 13.5
+//   64x32 in four stages, at most 256 tiles (one a CU)
+//     M = 96, N = 5120 (240 tiles) 7.2, 64x64 8.8;  M = 128 (320): 9.1, 8.9
+//     M = 333, N = 1000, K = 4096 (176) 11.1, 13.4
+//   64x64 in four stages, at most 256 tiles
+//     M = 192 (240 tiles) 9.2, 128x64 10.4;  M = 256 (320): 11.1, 10.8;
 //     grouped E = 8, M = 1024 (512): 23.3, 18.4
+//     (three stages: M = 333, N = 1000, K = 4096  14.3, four 13.4; with 64x32
+//     12.1 and 11.1; BF16, E = 8, M = 64  17.7 and 14.4)
 //   128x32, at most 32 rows (grouped: 16 a slot, which scatter about their mean)
-//     N = 32768, M = 32  14.6, 128x64 15.6;  E = 256, M = 64 (2 a slot): 90.8,
+//     N = 32768, M = 32  14.6, 128x64 15.1;  E = 256, M = 64 (2 a slot): 90.8,
 //     91.3;  M = 512 (16): 101.2, 101.4;  M = 1024 (32): 131, 109
 //   128x64, at most 512 tiles (two a CU), or grouped with less than 48 rows a slot
 //     M = 512 (320 tiles) 14.4, 256x128 17.9;  M = 1024 (640): 23.7, 19.7;
@@ -842,19 +850,19 @@ template <bool FP8, bool GROUPED, typename Y>
 int32_t launch_block_gemm(const BlockGemmParams& p, const char* what, hipStream_t s) {
   constexpr Mma kExact = FP8 ? Mma::kFp8Exact : Mma::kBf16;
   constexpr Mma kFast = FP8 && sizeof(Y) == 2 ? Mma::kFp8 : kExact;
-  constexpr int64_t kSmallTiles = 256, kMidTiles = 512;
   const int64_t per_slot = tiles_of(p.R, p.slots);  // mean rows of a slot (dense: all)
   auto tiles = [&](int n, int m) { return p.slots * tiles_of(per_slot, m) * tiles_of(p.N, n); };
-  if (tiles(16, 16) <= (GROUPED ? 1024 : 640) && !(GROUPED && per_slot > 8))
-    return launch_direct<kExact, GROUPED, Y>(p, what, s);
-  if (tiles(64, 64) <= kSmallTiles)
-    return launch_tiled<kFast, GROUPED, 64, 64, 2, 2, Y>(p, what, s);
+  const bool few = !GROUPED || per_slot <= 8;
+  const int64_t direct = kFast == Mma::kFp8Exact && per_slot <= 16 ? 1024 : 512;
+  if (few && tiles(16, 16) <= direct) return launch_direct<kExact, GROUPED, Y>(p, what, s);
+  if (tiles(64, 32) <= 256) return launch_tiled<kFast, GROUPED, 64, 32, 2, 2, 4, Y>(p, what, s);
+  if (tiles(64, 64) <= 256) return launch_tiled<kFast, GROUPED, 64, 64, 2, 2, 4, Y>(p, what, s);
   if (per_slot <= (GROUPED ? 16 : 32))
-    return launch_tiled<kFast, GROUPED, 128, 32, 4, 1, Y>(p, what, s);
+    return launch_tiled<kFast, GROUPED, 128, 32, 4, 1, 3, Y>(p, what, s);
   if constexpr (kFast != Mma::kFp8Exact)
-    if (tiles(128, 64) > kMidTiles && !(GROUPED && per_slot < 48))
-      return launch_tiled<kFast, GROUPED, 256, 128, 4, 2, Y>(p, what, s);
-  return launch_tiled<kFast, GROUPED, 128, 64, 2, 2, Y>(p, what, s);
+    if (tiles(128, 64) > 512 && !(GROUPED && per_slot < 48))
+      return launch_tiled<kFast, GROUPED, 256, 128, 4, 2, 3, Y>(p, what, s);
+  return launch_tiled<kFast, GROUPED, 128, 64, 2, 2, 3, Y>(p, what, s);
 }
 
 }  // namespace

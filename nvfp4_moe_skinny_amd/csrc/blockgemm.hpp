@@ -459,8 +459,8 @@ __global__ void __launch_bounds__(kDirectWaves * 64) direct_gemm_kernel(BlockGem
 //
 // A block multiplies tiles of BM rows and BN weight rows, wave tiles of
 // BN / WVN x BM / WVM. A k step of the BN + BM rows (128 bytes each, and the x
-// scales) is copied to one of three LDS stages by direct loads, 16 bytes a
-// lane, two steps ahead of its products. Piece c of row r lies at piece
+// scales) is copied to one of S LDS stages by direct loads, 16 bytes a lane,
+// S - 1 steps ahead of its products. Piece c of row r lies at piece
 // c ^ (r % 8) of the row's 128 bytes, so lanes that read the same piece of
 // neighbouring rows hit different banks (no bank conflict counted in the
 // loop); a copy's lanes are contiguous in LDS, so the exchange is made on the
@@ -469,14 +469,15 @@ __global__ void __launch_bounds__(kDirectWaves * 64) direct_gemm_kernel(BlockGem
 // Order within step k, for a wave with NT rows of MT product tiles: its first
 // operands (two weight and MT x operands, the scales) are already in
 // registers; weight operand i + 2 is read while row i is multiplied, and the
-// copies of step k + 2 go out between the products, into the stage of step
+// copies of step k + S - 1 go out between the products, into the stage of step
 // k - 1; before the last row, one barrier: step k + 1 is complete and nobody
 // reads this stage any more; during the last row the first operands of step
 // k + 1 replace those just used. So the matrix cores have work across the
 // barrier (with the barrier between the steps and the operands read after it:
 // grouped gate_up 2048 -> 1024 at M = 4 15.0 us, this way 13.0), and a copy has
 // more than a step to arrive (with two stages and one step: M = 16 53 us,
-// this way 44; more than three stages only cost blocks per CU).
+// this way 44). Three stages; four where a tile a CU is all there is (beside the
+// choice of tiles).
 //
 // With more tiles than the chip holds at once (MANY), a CU's worth of blocks
 // takes them in turn: the last two steps of a tile copy the first two of the
@@ -516,7 +517,7 @@ __device__ __forceinline__ void arrive() {
   __builtin_amdgcn_sched_barrier(0);
 }
 
-template <Mma MODE, bool GROUPED, int BN, int BM, int WVN, int WVM>
+template <Mma MODE, bool GROUPED, int BN, int BM, int WVN, int WVM, int S>
 struct Tiled {
   static constexpr bool FP8 = MODE != Mma::kBf16;
   static constexpr int kWaves = WVN * WVM, kThreads = kWaves * 64;
@@ -530,7 +531,9 @@ struct Tiled {
   static_assert(LA * 8 * kWaves == BN && LB * 8 * kWaves == BM, "rows split evenly over the waves");
   static_assert(kBlock8 % WN == 0, "a wave's weight rows share a scale block");
   static_assert(NT % 2 == 0, "the first weight operand of a step is always a[0]");
-  static_assert(3 * kStageBytes <= 160 * 1024, "the stages fit the LDS");
+  // copies that may be on their way when the next step is to be complete
+  static constexpr int kLater = (S - 2) * kCopies;
+  static_assert(S * kStageBytes <= 160 * 1024, "the stages fit the LDS");
 
   // What a lane copies: byte offsets of its rows (weights: from the tile's
   // first row; x: from the tile's first row, or of any row when gathered),
@@ -617,8 +620,8 @@ struct Tiled {
     }
   };
 
-  // One step, held by cur: its products, ahead(i) (copy i of the step two
-  // further on) between them, and the first operands of the next step, held by
+  // One step, held by cur: its products, ahead(i) (copy i of the step
+  // S - 1 further on) between them, and the first operands of the next step, held by
   // other. MASK: the step may end past K (k0, k1: masks of the lane's pieces). LAST:
   // no step follows, so there are no copies, barrier and first operands.
   // FP8: a tile's block sum is scaled into the result two instructions later,
@@ -653,7 +656,7 @@ struct Tiled {
       bg_f32x4 t[kLag + 1];
       static_for<NT * MT>([&](auto qc) {
         constexpr int q = qc, i = q / MT, j = q % MT, d = q - kLag;
-        if constexpr (!LAST && i == NT - 1 && j == 0) arrive<kCopies>();
+        if constexpr (!LAST && i == NT - 1 && j == 0) arrive<kLater>();
         Operand<MODE> ao;
         ao.set(a[i % 3]);
         t[q % (kLag + 1)] = block_mma<MODE>(ao, b[j]);
@@ -680,7 +683,7 @@ struct Tiled {
       constexpr int kParts = (int)(sizeof(Operand<MODE>::v) / sizeof(bg_bf16x8));
       static_for<NT>([&](auto ic) {
         constexpr int i = ic;
-        if constexpr (!LAST && i == NT - 1) arrive<kCopies>();
+        if constexpr (!LAST && i == NT - 1) arrive<kLater>();
         Operand<MODE> ao;
         ao.set(a[i % 3]);
         bg_f32x4 t[MT];
@@ -726,13 +729,13 @@ __device__ __forceinline__ void pack4(const bg_f32x4& v, float* dst) {
   *reinterpret_cast<bg_f32x4*>(dst) = v;
 }
 
-template <Mma MODE, bool GROUPED, int BN, int BM, int WVN, int WVM>
+template <Mma MODE, bool GROUPED, int BN, int BM, int WVN, int WVM, int S>
 struct TiledLds {
-  using T = Tiled<MODE, GROUPED, BN, BM, WVN, WVM>;
+  using T = Tiled<MODE, GROUPED, BN, BM, WVN, WVM, S>;
   static constexpr int kScaleRows = T::FP8 ? (BN + kBlock8 - 1) / kBlock8 : 0;
   static constexpr int kScaleBytes = kScaleRows * 256;
   static constexpr int kPairBytes = GROUPED ? (BM + 63) / 64 * 256 : 0;
-  static constexpr int kPairs = 3 * T::kStageBytes;           // the pairs of three tiles
+  static constexpr int kPairs = S * T::kStageBytes;           // the pairs of three tiles
   static constexpr int kScales = kPairs + 3 * kPairBytes;     // and 64 weight scales a row
   static constexpr int kSlots = kScales + 3 * kScaleBytes;
   static constexpr int kBytes = kSlots + (GROUPED ? 64 * (int)sizeof(SlotTiles<BM>) : 0);
@@ -743,12 +746,13 @@ struct TiledLds {
   static_assert(kPerCu >= 1, "fits the LDS");
 };
 
-template <Mma MODE, bool GROUPED, int BN, int BM, int WVN, int WVM, bool MANY, typename Y>
+template <Mma MODE, bool GROUPED, int BN, int BM, int WVN, int WVM, int S, bool MANY, typename Y>
 __global__ void __launch_bounds__(WVN* WVM * 64,
-                                  (TiledLds<MODE, GROUPED, BN, BM, WVN, WVM>::kWavesPerSimd))
+                                  (TiledLds<MODE, GROUPED, BN, BM, WVN, WVM, S>::kWavesPerSimd))
     tiled_gemm_kernel(BlockGemmParams p, int n_tiles, uint32_t limit) {
-  using T = Tiled<MODE, GROUPED, BN, BM, WVN, WVM>;
-  using L = TiledLds<MODE, GROUPED, BN, BM, WVN, WVM>;
+  using T = Tiled<MODE, GROUPED, BN, BM, WVN, WVM, S>;
+  using L = TiledLds<MODE, GROUPED, BN, BM, WVN, WVM, S>;
+  static_assert(!MANY || S == 3, "a tile starts two steps before the last one ends");
   __shared__ __align__(1024) uint8_t stages[L::kBytes];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -873,18 +877,18 @@ __global__ void __launch_bounds__(WVN* WVM * 64,
   };
   auto after = [](uint32_t stage) {
     stage += T::kStageBytes;
-    return stage == 3 * T::kStageBytes ? 0u : stage;
+    return stage == S * T::kStageBytes ? 0u : stage;
   };
   // While a tile's steps run, the next one's pairs and scales are in LDS, and
   // from the last but one step on its copies are made; the one after that is
   // looked up in the last step, and put into LDS before the results, where the
   // wave waits for its copies anyway. With one or two steps a tile starts afresh.
-  uint32_t cur = 0, fill = 2 * T::kStageBytes;
+  uint32_t cur = 0, fill = (S - 1) * T::kStageBytes;
   auto start = [&](const Work& k, int third) {
     enter(k, third);
     cur = 0;
-    fill = 2 * T::kStageBytes;
-    static_for<2>([&](auto q) {
+    fill = (S - 1) * T::kStageBytes;
+    static_for<S - 1>([&](auto q) {
       static_for<T::kCopies>(
           [&](auto v) { T::template copy<v>(rows, c, wave, stages + q * T::kStageBytes); });
       c.advance(p, piece);
@@ -918,7 +922,7 @@ __global__ void __launch_bounds__(WVN* WVM * 64,
         start(work, third);
       }
       first = false;
-      arrive<T::kCopies>();
+      arrive<T::kLater>();
       f.read_a(stages, at);
       static_for<T::MT>([&](auto j) { f.template read_b<j>(stages, at); });
       f.read_xs(stages, at);
