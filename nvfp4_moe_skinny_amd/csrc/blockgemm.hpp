@@ -229,11 +229,16 @@ __device__ __forceinline__ int count_tiles(const BlockGemmParams& p, const SlotT
   return total;
 }
 
-// Row tile t of the slots' tiles in slot order (t uniform; the whole wave active).
+// The slot that holds row tile t of the slots' tiles in slot order.
+struct SlotAt {
+  int e, start, end;  // expert, its positions in pairs
+  int tiles, rel;     // its row tiles, t among them
+};
+
+// (t uniform, below count_tiles; the whole wave active)
 template <int BM>
-__device__ __forceinline__ RowTile find_tile(const BlockGemmParams& p, const SlotTiles<BM>& first,
-                                             int t, int lane) {
-  RowTile r = {0, 0, 0};
+__device__ __forceinline__ SlotAt find_slot(const BlockGemmParams& p, const SlotTiles<BM>& first,
+                                            int t, int lane) {
   for (int base = 0; base < p.slots; base += 256) {
     SlotTiles<BM> st = first;
     if (base > 0) st.load(p, base, lane);
@@ -242,25 +247,23 @@ __device__ __forceinline__ RowTile find_tile(const BlockGemmParams& p, const Slo
     if (t < total) {
       int rel = t - (incl - st.sum);  // < 0: an earlier lane's, >= sum: a later one's
       const unsigned long long hit = __ballot(rel >= 0 && rel < st.sum);
-      int e = 0, row0 = 0, rows = 0;
+      SlotAt s = {0, 0, 0, 1, 0};
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        if (rel >= 0 && rel < st.n[j]) {
-          e = st.e[j];
-          row0 = st.off[j] + rel * BM;
-          rows = min(st.off[j + 1] - row0, BM);
-        }
+        if (rel >= 0 && rel < st.n[j]) s = {st.e[j], st.off[j], st.off[j + 1], st.n[j], rel};
         rel -= st.n[j];
       }
       const int src = (int)__builtin_ctzll(hit);
-      r.e = __builtin_amdgcn_readlane(e, src);
-      r.row0 = __builtin_amdgcn_readlane(row0, src);
-      r.rows = __builtin_amdgcn_readlane(rows, src);
-      return r;
+      s.e = __builtin_amdgcn_readlane(s.e, src);
+      s.start = __builtin_amdgcn_readlane(s.start, src);
+      s.end = __builtin_amdgcn_readlane(s.end, src);
+      s.tiles = __builtin_amdgcn_readlane(s.tiles, src);
+      s.rel = __builtin_amdgcn_readlane(s.rel, src);
+      return s;
     }
     t -= total;
   }
-  return r;
+  return {0, 0, 0, 1, 0};
 }
 
 // A block's work: a row tile and the first of its weight rows.
@@ -271,12 +274,15 @@ struct Work {
 
 // The block's tiles. Blocks are handed to the eight XCDs in turn (block b to
 // XCD b % 8), each with its own L2, so XCD x gets the consecutive part
-// [x T / 8, (x + 1) T / 8) of the T tiles, in bands of eight row tiles: within a
-// band all row tiles of one column of weight rows, then the next column. The
-// blocks an XCD runs at a time then share row tiles and weight rows about
-// equally, and an expert's weights stay on one XCD or two. The XCD's blocks
-// take its tiles in turn; a block past its XCD's part has none. T counts at
-// most the tiles that `limit` (the host's bound) allows, whatever off holds.
+// [x T / 8, (x + 1) T / 8) of the T tiles, and its blocks take those in turn; a
+// block past its XCD's part has none. The order is slot by slot, a slot (or the
+// dense rows) in bands of eight row tiles: within a band all row tiles of one
+// column of weight rows, then the next column. The blocks that an XCD runs at a
+// time then share row tiles and weight rows about equally, and read an expert's
+// weights together (bands across slots cut at every eighth row tile, and half an
+// expert's weights came again: grouped gate_up at M = 8192 read 955 MB, @@).
+// T counts at most the tiles that `limit` (the host's bound) allows, whatever
+// off holds.
 template <int BN, int BM, bool GROUPED>
 struct BlockTiles {
   static constexpr int kBand = 8;
@@ -301,16 +307,20 @@ struct BlockTiles {
                                        int lane) {
     Work w = {{0, 0, 0}, 0};
     if (q >= end) return w;
+    SlotAt slot = {0, 0, p.R, m_tiles, 0};
+    uint32_t at = q;  // among the slot's tiles
+    if constexpr (GROUPED) {
+      const uint32_t t = q / (uint32_t)n_tiles;
+      slot = find_slot<BM>(p, first, (int)t, lane);
+      at = q - (t - (uint32_t)slot.rel) * (uint32_t)n_tiles;
+    }
     const uint32_t per_band = kBand * (uint32_t)n_tiles;
-    const uint32_t band = q / per_band, in = q - band * per_band;
-    const uint32_t rows = min((uint32_t)kBand, (uint32_t)m_tiles - band * kBand);
+    const uint32_t band = at / per_band, in = at - band * per_band;
+    const uint32_t rows = min((uint32_t)kBand, (uint32_t)slot.tiles - band * kBand);
     const uint32_t n = in / rows;
-    const int m = (int)(band * kBand + (in - n * rows));
+    const int row0 = slot.start + (int)(band * kBand + (in - n * rows)) * BM;
     w.n0 = (int)n * BN;
-    if constexpr (GROUPED)
-      w.t = find_tile<BM>(p, first, m, lane);
-    else
-      w.t = {0, m * BM, min(p.R - m * BM, BM)};
+    w.t = {slot.e, row0, min(slot.end - row0, BM)};
     q += gridDim.x >> 3;
     return w;
   }
