@@ -280,7 +280,8 @@ struct Work {
 // column of weight rows, then the next column. The blocks that an XCD runs at a
 // time then share row tiles and weight rows about equally, and read an expert's
 // weights together (bands across slots cut at every eighth row tile, and half an
-// expert's weights came again: grouped gate_up at M = 8192 read 955 MB, @@).
+// expert's weights came again: grouped gate_up at M = 8192 read 955 MB, this way
+// 795, of 688 with the results).
 // T counts at most the tiles that `limit` (the host's bound) allows, whatever
 // off holds.
 template <int BN, int BM, bool GROUPED>
@@ -495,15 +496,18 @@ __global__ void __launch_bounds__(kDirectWaves * 64) direct_gemm_kernel(BlockGem
 // results stand between two tiles (one tile a block: M = 8192, 2048 -> 5120
 // 98.6 us, this way 93.6; grouped gate_up, E = 256, M = 8192 265 and 241).
 //
-// What bounds large products (93.6 us, 1.84 PFLOP/s): LDS. A 256 x 128 step is
-// 48 direct loads of 1 KB, about 24 clocks of the LDS each beside reads, and
-// 128 KB of operand reads at about 230 bytes a clock, 0.86 us of the step's 1.1;
-// its matrix instructions alone take 0.67 (through registers and LDS stores it
-// took the same time; 256 x 256 tiles have a third fewer bytes, but only two
-// stages fit: 93.7 with one tile a block). Grouped products read their weights
-// from HBM beside that (241 us: 2.9 TB/s, and rows that end inside a tile cost a
-// quarter of the products); with few rows a slot those bytes are the bound
-// (M = 256 98 us, 5.5 TB/s).
+// What bounds large products (M = 8192, 2048 -> 5120: 90 to 94 us by the card's
+// clock, 1.83 to 1.9 PFLOP/s, 47 % of the cycles matrix instructions): LDS. A
+// 256 x 128 step is 48 direct loads of 1 KB, about 24 clocks of the LDS each
+// beside reads, and 128 KB of operand reads at about 230 bytes a clock, 0.86 us
+// of the step's 1.1; its matrix instructions alone take 0.67 (through registers
+// and LDS stores it took the same time; 256 x 256 tiles have a third fewer
+// bytes, but only two stages fit: 93.7 with one tile a block). Grouped products
+// of some hundred rows an expert (M = 8192: 239 us, 1.15 PFLOP/s): a quarter of
+// the tiles' rows are empty, and every step's weights come from HBM, two steps
+// ahead and no more, for that is what LDS holds (eight experts of 8192 rows, the
+// same products: 176 us). With few rows a slot the bytes of the weights
+// are the bound (M = 256 98 us, 5.5 TB/s).
 typedef __attribute__((address_space(3))) void lds_void;
 typedef const __attribute__((address_space(1))) void global_void;
 
@@ -724,6 +728,21 @@ struct Tiled {
       });
     }
   }
+
+  // A step of a wave whose rows all lie past the tile's last: its copies only,
+  // and in a tile's last step (MASK) the first operands of what follows.
+  template <bool MASK, bool LAST, typename Ahead>
+  static __device__ __forceinline__ void idle(const uint8_t* other, const Place& at, First& f,
+                                              Ahead ahead) {
+    if constexpr (LAST) return;
+    static_for<kCopies>([&](auto v) { ahead(v); });
+    arrive<kLater>();
+    if constexpr (MASK) {
+      f.read_a(other, at);
+      static_for<MT>([&](auto j) { f.template read_b<j>(other, at); });
+      f.read_xs(other, at);
+    }
+  }
 };
 
 __device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
@@ -879,10 +898,18 @@ __global__ void __launch_bounds__(WVN* WVM * 64,
 
   bg_f32x4 acc[T::NT][T::MT];
   typename T::First f;
-  auto step = [&](auto mask, auto last, int kb, uint32_t k0, uint32_t k1, const uint8_t* __restrict__ cur,
-                  const uint8_t* __restrict__ next, uint8_t* __restrict__ fill) {
-    T::template step<mask, last>(cur, next, at, f, ws_of(kb), k0, k1, acc,
-                           [&](auto v) { T::template copy<v>(rows, c, wave, fill); });
+  // Some of the wave's rows are the tile's; a wave without any leaves the
+  // products to the others (grouped gate_up, E = 256, M = 2048, 64 rows a slot:
+  // 131.5 us, this way 127).
+  bool busy = true;
+  auto step = [&](auto mask, auto last, int kb, uint32_t k0, uint32_t k1,
+                  const uint8_t* __restrict__ cur, const uint8_t* __restrict__ next,
+                  uint8_t* __restrict__ fill) {
+    auto copies = [&](auto v) { T::template copy<v>(rows, c, wave, fill); };
+    if (!MANY || WVM == 1 || busy)
+      T::template step<mask, last>(cur, next, at, f, ws_of(kb), k0, k1, acc, copies);
+    else
+      T::template idle<mask, last>(next, at, f, copies);
     c.advance(p, piece);
   };
   auto after = [](uint32_t stage) {
@@ -938,6 +965,7 @@ __global__ void __launch_bounds__(WVN* WVM * 64,
       f.read_xs(stages, at);
     }
     flowing = MANY && ahead.t.rows > 0 && p.KB > 2;
+    busy = wm < work.t.rows;
 #pragma unroll
     for (int i = 0; i < T::NT; ++i)
 #pragma unroll
@@ -946,7 +974,8 @@ __global__ void __launch_bounds__(WVN* WVM * 64,
 #pragma unroll 1
     for (int kb = 0; kb + 1 < p.KB; ++kb) {
       if (flowing && kb + 2 == p.KB) enter(ahead, third1);
-      step(std::false_type{}, std::false_type{}, kb, ~0u, ~0u, stages + cur, stages + after(cur), stages + fill);
+      step(std::false_type{}, std::false_type{}, kb, ~0u, ~0u, stages + cur, stages + after(cur),
+           stages + fill);
       cur = after(cur);
       fill = after(fill);
     }
