@@ -281,7 +281,7 @@ struct Work {
 // time then share row tiles and weight rows about equally, and read an expert's
 // weights together (bands across slots cut at every eighth row tile, and half an
 // expert's weights came again: grouped gate_up at M = 8192 read 955 MB, this way
-// 795, of 688 with the results).
+// 800 to 870; every byte once: 554).
 // T counts at most the tiles that `limit` (the host's bound) allows, whatever
 // off holds.
 template <int BN, int BM, bool GROUPED>
