@@ -327,12 +327,13 @@ int32_t moe_nvfp4_route_decode_static(const moe_nvfp4_args* args, const float* l
  * x are ldx elements apart (ldx >= the row's columns). x_type BF16 or F32; x
  * 16-byte aligned, ldx a multiple of 16 bytes. A block that holds an infinity
  * or a NaN gets a scale that is not finite and the products of its row come
- * out NaN. One launch. */
+ * out NaN. M * ceil(K/128) <= 2^27. One launch. */
 int32_t fp8_quantize_rows(const void* x, int32_t x_type, int64_t M, int64_t K, int64_t ldx,
                           int32_t swiglu, uint8_t* codes, float* scales, hipStream_t stream);
 
 /* Quantizes weights x [G][N][K] (BF16 or F32, contiguous, 16-byte aligned):
- * the same recipe over 128 x 128 blocks. G = 0 does nothing. One launch. */
+ * the same recipe over 128 x 128 blocks, less than 2^24 of them. G = 0 does
+ * nothing. One launch. */
 int32_t fp8_quantize_blocks(const void* x, int32_t x_type, int64_t G, int64_t N, int64_t K,
                             uint8_t* codes, float* scales, hipStream_t stream);
 
@@ -395,7 +396,7 @@ int32_t moe_grouped_gemm(const moe_grouped_args* args, hipStream_t stream);
  * moe_grouped_gemm's y). y [M k][H] and shared [M][H] (or NULL) of type
  * y_type, w [M][k], residual BF16 [M][H] (or NULL; may be out). A pair whose
  * weight is 0 adds nothing, whatever its row of y holds. 1 <= k <= 8,
- * 1 <= H <= 2^20, M <= 2^24. One launch. */
+ * 1 <= H <= 2^20, M <= 2^24, M * H <= 2^31. One launch. */
 int32_t moe_combine(const void* y, int32_t y_type, const float* w, const void* shared,
                     const uint16_t* residual, int64_t M, int64_t k, int64_t H, uint16_t* out,
                     hipStream_t stream);

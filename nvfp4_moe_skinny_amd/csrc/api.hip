@@ -727,6 +727,7 @@ constexpr int64_t kBlockMaxN = (int64_t)1 << 20;
 constexpr int64_t kGroupedMaxE = 1024;
 constexpr int64_t kMaxGrid = ((int64_t)1 << 31) - 1;
 constexpr int64_t kBlockMaxOut = (int64_t)1 << 38;  // elements of y
+constexpr int64_t kMaxLanes = (int64_t)1 << 32;      // lanes of a launch, exclusive
 
 int32_t check_block_nk(int64_t N, int64_t K) {
   if (N < 1 || K < 1) return fail(NVFP4MOE_ERR_BAD_SHAPE, "N and K must be >= 1");
@@ -877,7 +878,8 @@ int32_t fp8_quantize_rows(const void* x, int32_t x_type, int64_t M, int64_t K, i
     return fail(NVFP4MOE_ERR_BAD_SHAPE, "swiglu must be 0 or 1 (got %d)", (int)swiglu);
   if (M < 0) return fail(NVFP4MOE_ERR_BAD_SHAPE, "M must be >= 0");
   if ((st = check_block_nk(1, K)) != NVFP4MOE_OK) return st;
-  if (M > kBlockMaxRows) return fail(NVFP4MOE_ERR_UNSUPPORTED, "M = %lld too large", (long long)M);
+  if (M > kBlockMaxRows || M * blocks128(K) > kMaxLanes / 32)  // 16 lanes a block
+    return fail(NVFP4MOE_ERR_UNSUPPORTED, "M = %lld: more than 2^27 blocks", (long long)M);
   const int64_t cols = swiglu ? 2 * K : K;
   if (ldx < cols || ldx > (int64_t)1 << 32)
     return fail(NVFP4MOE_ERR_BAD_SHAPE, "ldx = %lld: a row has %lld columns", (long long)ldx,
@@ -902,8 +904,8 @@ int32_t fp8_quantize_blocks(const void* x, int32_t x_type, int64_t G, int64_t N,
   if (G < 0) return fail(NVFP4MOE_ERR_BAD_SHAPE, "G must be >= 0");
   if ((st = check_block_nk(N, K)) != NVFP4MOE_OK) return st;
   const int64_t NB = blocks128(N), KB = blocks128(K);
-  if (G > kMaxG || G * NB * KB > kMaxGrid)
-    return fail(NVFP4MOE_ERR_UNSUPPORTED, "G = %lld: more than 2^31 - 1 blocks", (long long)G);
+  if (G > kMaxG || G * NB * KB * kQuantBlocksThreads >= kMaxLanes)
+    return fail(NVFP4MOE_ERR_UNSUPPORTED, "G = %lld: more than 2^24 - 1 blocks", (long long)G);
   if (G == 0) return ok();
   if (!x || !codes || !scales) return fail(NVFP4MOE_ERR_NULL_ARG, "fp8_quantize_blocks: null");
   if (!aligned(x, 16) || !aligned(codes, 16) || !aligned(scales, 4))
@@ -1062,8 +1064,8 @@ int32_t moe_combine(const void* y, int32_t y_type, const float* w, const void* s
     return fail(NVFP4MOE_ERR_BAD_SHAPE, "need M >= 0 and k, H >= 1");
   if (k > kRouteMaxK || M > kBlockMaxRows || H > kBlockMaxN)
     return fail(NVFP4MOE_ERR_UNSUPPORTED, "need k <= 8, M <= 2^24 and H <= 2^20");
-  if ((M * H + kCombineThreads - 1) / kCombineThreads > kMaxGrid)
-    return fail(NVFP4MOE_ERR_UNSUPPORTED, "moe_combine: grid too large");
+  if (M * H > kMaxLanes / 2)
+    return fail(NVFP4MOE_ERR_UNSUPPORTED, "moe_combine: M H = %lld > 2^31", (long long)(M * H));
   if (M == 0) return ok();
   if (!y || !w || !out) return fail(NVFP4MOE_ERR_NULL_ARG, "moe_combine: null");
   const uintptr_t el = (uintptr_t)type_bytes(y_type);

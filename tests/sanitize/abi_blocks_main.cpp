@@ -56,6 +56,12 @@ int main() {
   EXPECT(fp8_block_gemm(u8, f32, (int64_t)1 << 24, 128, u8, f32, (int64_t)1 << 20, f, BF,
                         (int64_t)1 << 20, nullptr),
          unsup);
+  // more lanes than a launch holds
+  EXPECT(fp8_quantize_rows(f, BF, (int64_t)1 << 20, 65536, 65536, 0, u8, f32, nullptr), unsup);
+  EXPECT(fp8_quantize_blocks(f, BF, 1 << 12, 128 * 64, 128 * 64, u8, f32, nullptr), unsup);
+  EXPECT(moe_combine(f, F32, f32, nullptr, nullptr, (int64_t)1 << 16, 1, ((int64_t)1 << 15) + 1,
+                     u16, nullptr),
+         unsup);
   EXPECT(fp8_quantize_rows(odd, BF, 4, 128, 128, 0, u8, f32, nullptr), unsup);
   EXPECT(fp8_quantize_rows(nullptr, BF, 4, 128, 128, 0, u8, f32, nullptr), null);
   EXPECT(fp8_quantize_rows(nullptr, BF, 0, 128, 128, 0, nullptr, nullptr, nullptr), NVFP4MOE_OK);

@@ -25,7 +25,7 @@ def test_quantize_rows_validation(m):
         assert call(**kw) == m.NVFP4MOE_ERR_BAD_SHAPE, kw
     for kw in (dict(K=24, ldx=24), dict(K=65552, ldx=65552), dict(M=(1 << 24) + 1),
                dict(M=1 << 60), dict(x=FAKE + 8), dict(codes=FAKE + 8), dict(scales=FAKE + 2),
-               dict(ldx=260), dict(t=1, ldx=258)):
+               dict(ldx=260), dict(t=1, ldx=258), dict(M=1 << 20, K=65536, ldx=65536)):
         assert call(**kw) == m.NVFP4MOE_ERR_UNSUPPORTED, kw
     assert m.last_error_detail()
     assert call(M=0, x=None, codes=None, scales=None) == m.NVFP4MOE_OK
@@ -40,7 +40,8 @@ def test_quantize_blocks_validation(m):
     for kw in (dict(t=2), dict(G=-1), dict(N=0), dict(K=0)):
         assert call(**kw) == m.NVFP4MOE_ERR_BAD_SHAPE, kw
     for kw in (dict(K=40), dict(K=1 << 17), dict(N=(1 << 20) + 1), dict(G=1 << 21),
-               dict(G=1 << 20, N=1 << 20, K=65536), dict(x=FAKE + 4), dict(codes=FAKE + 4),
+               dict(G=1 << 20, N=1 << 20, K=65536), dict(G=4096, N=8192, K=8192),
+               dict(x=FAKE + 4), dict(codes=FAKE + 4),
                dict(scales=FAKE + 1)):
         assert call(**kw) == m.NVFP4MOE_ERR_UNSUPPORTED, kw
     assert call(G=0, x=None, codes=None, scales=None) == m.NVFP4MOE_OK
@@ -102,7 +103,7 @@ def test_combine_validation(m):
         assert call(**kw) == m.NVFP4MOE_ERR_NULL_ARG, kw
     for kw in (dict(t=2), dict(M=-1), dict(k=0), dict(H=0)):
         assert call(**kw) == m.NVFP4MOE_ERR_BAD_SHAPE, kw
-    for kw in (dict(k=9), dict(M=(1 << 24) + 1), dict(H=(1 << 20) + 1), dict(M=1 << 24, H=1 << 20),
+    for kw in (dict(k=9), dict(M=(1 << 24) + 1), dict(H=(1 << 20) + 1), dict(M=1 << 16, H=(1 << 15) + 1),
                dict(y=FAKE + 1), dict(t=1, y=FAKE + 2), dict(w=FAKE + 2), dict(shared=FAKE + 1),
                dict(residual=FAKE + 1), dict(out=FAKE + 1)):
         assert call(**kw) == m.NVFP4MOE_ERR_UNSUPPORTED, kw

@@ -263,3 +263,41 @@ def test_other_stream(m, gpu):
     b = m.fp8_block_gemm(m.fp8_quantize_rows(x, stream=st), w, stream=st)
     st.synchronize()
     assert torch.equal(a, b)
+
+
+def test_offsets_past_32_bits(m, gpu):
+    """Rows and results whose offsets pass 2^31 elements and 2^32 bytes: the last
+    rows are those of a call on them alone."""
+    g = torch.Generator(device=gpu).manual_seed(3)
+    M, K = 270000, 8192
+    x = torch.empty((M, K), dtype=torch.bfloat16, device=gpu)
+    x[:-7].fill_(1.0)
+    x[-7:] = torch.randn((7, K), generator=g, device=gpu).to(torch.bfloat16)
+    q, q7 = m.fp8_quantize_rows(x), m.fp8_quantize_rows(x[-7:])
+    assert torch.equal(q.codes[-7:], q7.codes) and torch.equal(q.scales[:, -7:], q7.scales)
+    assert torch.equal(q.codes[0], m.fp8_quantize_rows(x[:1]).codes[0])
+    # the codes as operand: 2.2 GB of x; then 2.3e9 results
+    w = m.fp8_quantize_blocks(torch.randn((1, 40, K), generator=g, device=gpu))
+    y = m.fp8_block_gemm(q, w, out_dtype=torch.float32)
+    y7 = m.fp8_block_gemm(q7, w, out_dtype=torch.float32)
+    x64, w64 = ref.dequant_rows(q7), ref.dequant_blocks(w)[0]
+    r, mag = ref.gemm_f64(x64, w64)
+    for got in (y[-7:], y7):
+        ref.assert_close(got, r, ref.gemm_tol(r, mag, K, False))
+    del q, x, y
+    M, N, K = 140000, 16400, 128
+    ints = lambda *s: torch.randint(-4, 5, s, generator=g, device=gpu).to(torch.float8_e4m3fn)
+    xc, wc = ints(M, K), ints(1, N, K)
+    ones = lambda *s: torch.ones(s, device=gpu)
+    y = m.fp8_block_gemm(m.Fp8Rows(xc.view(torch.uint8), ones(1, M)),
+                         m.Fp8Blocks(wc.view(torch.uint8), ones(1, ref.nblk(N), 1)))
+    for rows in (slice(0, 5), slice(M // 2, M // 2 + 5), slice(M - 5, M)):
+        want = torch.mm(xc[rows].double(), wc[0].double().t().contiguous())
+        assert torch.equal(y[rows], want.to(torch.bfloat16))
+    # a weight of 4.9 GB
+    G, N, K = 300, 4000, 2048
+    wb = torch.empty((G, N, K), dtype=torch.bfloat16, device=gpu)
+    wb[:-1].fill_(1.0)
+    wb[-1] = torch.randn((N, K), generator=g, device=gpu).to(torch.bfloat16)
+    q, q1 = m.fp8_quantize_blocks(wb), m.fp8_quantize_blocks(wb[-1])
+    assert torch.equal(q.codes[-1:], q1.codes) and torch.equal(q.scales[-1:], q1.scales)

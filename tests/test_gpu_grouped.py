@@ -398,3 +398,46 @@ def test_two_streams_at_once(m, gpu):
     torch.cuda.synchronize()
     for i in range(2):
         assert all(torch.equal(g, want[i]) for g in got[i])
+
+
+@pytest.mark.parametrize("typ", ["fp8", "bf16"])
+@pytest.mark.parametrize("M", [2, 400])
+def test_offsets_past_32_bits(m, gpu, typ, M):
+    """Experts whose weights lie past 2^32 bytes, and pairs whose results do."""
+    E, k, N, K = 1000, 4, 4608, 1024 if typ == "fp8" else 512
+    g = torch.Generator(device=gpu).manual_seed(M)
+    ints = lambda *s: torch.randint(-4, 5, s, generator=g, device=gpu)
+    if typ == "fp8":
+        codes = lambda *s: ints(*s).to(torch.float8_e4m3fn).view(torch.uint8)
+        w = m.Fp8Blocks(codes(1, N, K).repeat(E, 1, 1), torch.ones((E, N // 128, K // 128), device=gpu))
+        w.scales *= 2.0 ** (torch.arange(E, device=gpu) % 5).view(E, 1, 1)
+        x = m.Fp8Rows(codes(M, K), torch.ones((K // 128, M), device=gpu))
+        w64 = lambda e: ref.e4m3_values(w.codes[e]).to(gpu) * 2.0 ** (e % 5)
+        x64 = ref.e4m3_values(x.codes).to(gpu)
+        assert w.codes.numel() > 2 ** 32
+    else:
+        w = ints(1, N, K).to(torch.bfloat16).repeat(E, 1, 1)
+        w *= (2.0 ** (torch.arange(E, device=gpu) % 5)).to(torch.bfloat16).view(E, 1, 1)
+        x = ints(M, K).to(torch.bfloat16)
+        w64, x64 = (lambda e: w[e].double()), x.double()
+        assert w.numel() * 2 > 2 ** 32
+    ids = E - 1 - _ids(M, M, 40, k, "even")
+    r = ref.routing_of(m, ids, E, gpu)
+    y = torch.zeros((M * k, 1500000 if M == 400 else N), dtype=torch.bfloat16, device=gpu)[:, :N]
+    m.moe_grouped_gemm(x, r, w, out=y)
+    flat = ids.reshape(-1).to(gpu)
+    for e in sorted(set(ids.reshape(-1).tolist())):
+        p = (flat == e).nonzero().reshape(-1)
+        want = torch.mm(x64[p // k], w64(e).t().contiguous())
+        assert torch.equal(y[p], want.to(torch.bfloat16)), e
+
+
+def test_combine_offsets_past_32_bits(m, gpu):
+    M, k, H = 70000, 8, 4096
+    g = torch.Generator(device=gpu).manual_seed(1)
+    y = torch.empty((M * k, H), dtype=torch.bfloat16, device=gpu).fill_(1.0)
+    y[-5 * k:] = torch.randn((5 * k, H), generator=g, device=gpu).to(torch.bfloat16)
+    w = torch.rand((M, k), generator=g, device=gpu)
+    out = m.moe_combine(y, w)
+    assert torch.equal(out[-5:], m.moe_combine(y[-5 * k:], w[-5:].contiguous()))
+    assert torch.equal(out[:5], m.moe_combine(y[:5 * k], w[:5].contiguous()))
