@@ -103,7 +103,8 @@ def test_combine_validation(m):
         assert call(**kw) == m.NVFP4MOE_ERR_NULL_ARG, kw
     for kw in (dict(t=2), dict(M=-1), dict(k=0), dict(H=0)):
         assert call(**kw) == m.NVFP4MOE_ERR_BAD_SHAPE, kw
-    for kw in (dict(k=9), dict(M=(1 << 24) + 1), dict(H=(1 << 20) + 1), dict(M=1 << 16, H=(1 << 15) + 1),
+    for kw in (dict(k=9), dict(M=(1 << 24) + 1), dict(H=(1 << 20) + 1),
+               dict(M=1 << 16, H=(1 << 15) + 1),
                dict(y=FAKE + 1), dict(t=1, y=FAKE + 2), dict(w=FAKE + 2), dict(shared=FAKE + 1),
                dict(residual=FAKE + 1), dict(out=FAKE + 1)):
         assert call(**kw) == m.NVFP4MOE_ERR_UNSUPPORTED, kw

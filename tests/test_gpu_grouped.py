@@ -334,7 +334,8 @@ def test_chain(m, gpu, M, E, k, H, I):
     torch.cuda.synchronize()
     ids = c["r"].ids.cpu().long()
     f = lambda q: ref.dequant_rows(q)
-    for x, w, y, K, pp in ((c["xq"], d["gu"], c["u"], H, False), (c["h"], d["dn"], c["y"], I, True)):
+    for x, w, y, K, pp in ((c["xq"], d["gu"], c["u"], H, False),
+                           (c["h"], d["dn"], c["y"], I, True)):
         want, mag, _ = ref.grouped_f64(f(x), ref.dequant_blocks(w), ids, pp)
         ref.assert_close(y, want, ref.gemm_tol(want, mag, K, False))
     for x, w, y, K in ((c["xq"], d["sgu"], c["su"], H), (c["sh"], d["sdn"], c["sy"], I)):
@@ -409,7 +410,8 @@ def test_offsets_past_32_bits(m, gpu, typ, M):
     ints = lambda *s: torch.randint(-4, 5, s, generator=g, device=gpu)
     if typ == "fp8":
         codes = lambda *s: ints(*s).to(torch.float8_e4m3fn).view(torch.uint8)
-        w = m.Fp8Blocks(codes(1, N, K).repeat(E, 1, 1), torch.ones((E, N // 128, K // 128), device=gpu))
+        w = m.Fp8Blocks(codes(1, N, K).repeat(E, 1, 1),
+                        torch.ones((E, N // 128, K // 128), device=gpu))
         w.scales *= 2.0 ** (torch.arange(E, device=gpu) % 5).view(E, 1, 1)
         x = m.Fp8Rows(codes(M, K), torch.ones((K // 128, M), device=gpu))
         w64 = lambda e: ref.e4m3_values(w.codes[e]).to(gpu) * 2.0 ** (e % 5)
@@ -441,3 +443,43 @@ def test_combine_offsets_past_32_bits(m, gpu):
     out = m.moe_combine(y, w)
     assert torch.equal(out[-5:], m.moe_combine(y[-5 * k:], w[-5:].contiguous()))
     assert torch.equal(out[:5], m.moe_combine(y[:5 * k], w[:5].contiguous()))
+
+
+@pytest.mark.parametrize("typ", ["fp8", "bf16"])
+def test_large_products_in_graphs_on_two_streams(m, gpu, typ):
+    """Two graphs of products with more tiles than blocks, replayed at once on two
+    streams with new routing and rows each time, against eager calls."""
+    M, E, k, N, K = 1200, 64, 4, 1100, 400
+    x, w, _, _ = _operands(m, gpu, 5, typ, M, E, N, K)
+    r = ref.routing_of(m, _ids(0, M, E, k, "even"), E, gpu)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    graphs, outs = [], []
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+        out = torch.zeros((M * k, N), dtype=torch.bfloat16, device=gpu)
+        with torch.cuda.stream(s):
+            m.moe_grouped_gemm(x, r, w, out=out)
+        s.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            m.moe_grouped_gemm(x, r, w, out=out)
+        graphs.append(g)
+        outs.append(out)
+    for rep in range(4):
+        how = ("skewed", "even", "one", "skewed")[rep]
+        new = ref.routing_of(m, _ids(rep + 1, M, E, k, how), E, gpu)
+        for a, b in zip((r.pairs, r.active, r.active_offsets, r.n_active),
+                        (new.pairs, new.active, new.active_offsets, new.n_active)):
+            a.copy_(b)
+        xc = x.codes if typ == "fp8" else x
+        xc.copy_(xc.roll(rep + 1, 0))
+        for o in outs:
+            o.zero_()
+        torch.cuda.synchronize()
+        for s, g in zip(streams, graphs):
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        want = m.moe_grouped_gemm(x, r, w)
+        for o in outs:
+            assert torch.equal(o, want), rep
