@@ -496,8 +496,8 @@ __global__ void __launch_bounds__(kDirectWaves * 64) direct_gemm_kernel(BlockGem
 // results stand between two tiles (one tile a block: M = 8192, 2048 -> 5120
 // 98.6 us, this way 93.6; grouped gate_up, E = 256, M = 8192 265 and 241).
 //
-// What bounds large products (M = 8192, 2048 -> 5120: 90 to 94 us by the card's
-// clock, 1.83 to 1.9 PFLOP/s, 47 % of the cycles matrix instructions): LDS. A
+// What bounds large products (M = 8192, 2048 -> 5120: 90 to 97 us by the card's
+// clock, 1.77 to 1.9 PFLOP/s, 46 % of the cycles matrix instructions): LDS. A
 // 256 x 128 step is 48 direct loads of 1 KB, about 24 clocks of the LDS each
 // beside reads, and 128 KB of operand reads at about 230 bytes a clock, 0.86 us
 // of the step's 1.1; its matrix instructions alone take 0.67 (through registers
