@@ -200,7 +200,8 @@ def test_block_gemm_integers_exact(m, gpu, M, N, K):
 
 
 @pytest.mark.parametrize("K", [16, 144, 272, 400, 8320])
-@pytest.mark.parametrize("M,N", [(2176, 4112), (2300, 4000), (5000, 1300)])
+@pytest.mark.parametrize("M,N", [(2176, 4112), (2300, 4000), (5000, 1300), (300, 33000),
+                                 (9000, 1300)])
 def test_block_gemm_more_tiles_than_blocks(m, gpu, M, N, K):
     """Blocks that take several tiles in turn, with one to four k steps and with
     more than 64: integers up to 4 (8320 products of at most 16: exact in FP32)."""

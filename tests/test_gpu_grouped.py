@@ -97,7 +97,7 @@ def test_grouped_integers_exact(m, gpu, typ, M, N, K):
 @pytest.mark.parametrize("K", [16, 144, 272, 400])
 @pytest.mark.parametrize("M,E,k,N,how", [
     (600, 300, 4, 260, "even"), (1500, 200, 4, 260, "skewed"), (2000, 40, 4, 520, "even"),
-    (4000, 300, 4, 260, "skewed")])
+    (4000, 300, 4, 260, "skewed"), (4100, 8, 2, 1300, "even"), (3000, 4, 2, 2100, "skewed")])
 def test_grouped_more_tiles_than_blocks(m, gpu, typ, K, M, E, k, N, how):
     """Blocks that take several tiles in turn, of every tile shape, with one k
     step and more, up to 300 slots (a wave holds 256 at a time): exact integers."""
